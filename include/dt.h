@@ -389,7 +389,149 @@ DT_API int dt_attn_cfg_shared(const dt_plan_params* p, const uint8_t* d_plan,
  * DT_ERR_INVALID (bad params, unknown kind, odd H for DT_SHARE_CFG). */
 DT_API int dt_plan_share_counts(const dt_plan_params* p, int32_t kind, dt_plan* io);
 
-/* Limit, in nanoseconds, of every bounded wait inside the fused kernel
+/* ---- block-sparse attention, and the passes in front of it -----------------
+ *
+ * A layer that attends sparsely computes, for each 128-row query block, only
+ * the key blocks that a cheap score selects:
+ *   dt_rope_table        cos/sin of the token positions, once per geometry;
+ *   dt_qk_norm_rope      per-head RMS norm and position rotation of queries
+ *                        and keys, token-major to head-major layout, and the
+ *                        block means of the results, in one pass;
+ *   dt_block_select      lists of key blocks by the scores of block means;
+ *   dt_attn_block_sparse attention over the lists: a state (OUT, LSE).
+ * Inference only: none of these has a gradient.  They run on the calling
+ * thread's current device, to which every buffer and the stream belong. */
+
+#define DT_TYPE_BF16 0
+#define DT_TYPE_F16  1
+#define DT_TYPE_F32  2
+
+/* Element strides of a [head][row][D] tensor whose D elements are contiguous:
+ * element (h, s, d) lives at h*head + s*row + d.  Dense head-major is
+ * {S*D, D}; a token-major [S][heads][D] tensor is {D, heads*D}. */
+typedef struct { int64_t head, row; } dt_strides;
+
+#define DT_ROPE_MAX_AXES 4
+typedef struct {
+  int32_t S;                    /* tokens */
+  int32_t n_axes;               /* position axes, 1 .. DT_ROPE_MAX_AXES */
+  int32_t dim[DT_ROPE_MAX_AXES];/* rotated dimensions of each axis: even, > 0, sum rot <= 256 */
+  double base;                  /* frequency base, > 0 (10000 is usual) */
+} dt_rope_params;
+
+/* Rotation table: pair i of axis a (j-th pair of that axis, axes in order) of
+ * token s turns by pos[a][s] * base^(-2 j / dim[a]); table[s][i] = (cos, sin).
+ * Angles are formed and reduced in 64 bits, so far positions keep their
+ * fraction.
+ *   pos     int32 [n_axes][S] (device, read; any sign)
+ *   table   fp32 [S][rot/2][2] (device, written)
+ * One launch, HBM-bound.  S = 0 launches nothing.  Errors: DT_ERR_INVALID,
+ * DT_ERR_UNSUPPORTED (misaligned pointer), DT_ERR_CUDA. */
+DT_API int dt_rope_table(const dt_rope_params* p, const int32_t* pos, float* table, void* stream);
+
+#define DT_ROPE_INTERLEAVED 0   /* rotation pairs (2i, 2i+1) */
+#define DT_ROPE_HALVES      1   /* rotation pairs (i, i + rot/2) */
+
+typedef struct {
+  int32_t S, D;                 /* tokens; head dim, a multiple of 8, 8 .. 128 */
+  int32_t H, Hkv;               /* query heads; key (and value) heads */
+  int32_t rot;                  /* leading dimensions rotated: a multiple of 8, 0 .. D (0: none) */
+  int32_t pairing;              /* DT_ROPE_* */
+  int32_t in_type, out_type;    /* DT_TYPE_*; out_type is in_type or DT_TYPE_BF16 */
+  int32_t norm;                 /* 1: RMS norm of every query and key row, 0: none */
+  int32_t q_block, k_block;     /* rows per block mean of queries / keys: 64 or 128 */
+  float eps;                    /* norm: y = x / sqrt(mean(x^2) + eps) * w; >= 0 */
+  dt_strides q_in, k_in, v_in, q_out, k_out, v_out;
+} dt_norm_rope_params;
+
+/* Per-head RMS norm, rotation, layout change and block means in one pass over
+ * the projections' output.  Every query and key row is normalised (norm = 1)
+ * and scaled by its weights, then its first rot dimensions are rotated by the
+ * token's table row: (a, b) -> (a cos - b sin, a sin + b cos).  Values pass
+ * through (converted).  Arithmetic in fp32, one rounding to out_type.
+ *   q, k, v     inputs [heads][S][D] with strides q_in, k_in, v_in.  Each may
+ *               be NULL (that part is skipped, with its outputs NULL too)
+ *   wq, wk      fp32 [D] norm weights; NULL = ones.  Not read with norm = 0
+ *   table       fp32 [S][rot/2][2] of dt_rope_table; not read with rot = 0
+ *   Q, K, V     outputs with strides q_out, k_out, v_out.  Q and K may be
+ *               NULL where their mean is wanted alone.  An output may be its
+ *               own input in place (same pointer, strides and type); other
+ *               overlaps are not allowed
+ *   q_mean      fp32 [H][ceil(S/q_block)][D] or NULL: mean of each block of
+ *               consecutive rows (the last block: of the rows it has), of the
+ *               values before the rounding to out_type
+ *   k_mean      fp32 [Hkv][ceil(S/k_block)][D] or NULL
+ * Row starts must be 16-byte aligned (pointers and strides); strides >= 0.
+ * S = 0 launches nothing.  One launch, HBM-bound.  Errors: DT_ERR_INVALID,
+ * DT_ERR_UNSUPPORTED (alignment, types), DT_ERR_CUDA. */
+DT_API int dt_qk_norm_rope(const dt_norm_rope_params* p, const void* q, const void* k, const void* v,
+                    const float* wq, const float* wk, const float* table,
+                    void* Q, void* K, void* V, float* q_mean, float* k_mean, void* stream);
+
+#define DT_SELECT_MAX_BLOCKS 16384
+typedef struct {
+  int32_t H, Hkv;               /* query heads; key heads: query head h reads key head h / (H/Hkv) */
+  int32_t nq, nk;               /* query blocks, key blocks (nk <= DT_SELECT_MAX_BLOCKS) */
+  int32_t D;                    /* a multiple of 4, 4 .. 128 */
+  int32_t topk;                 /* entries per list, >= 1 */
+  int32_t keep_first, keep_last;/* the first and last key blocks that every list holds; sum <= topk */
+  double margin;                /* >= 0; INFINITY: none */
+} dt_select_params;
+
+/* Key blocks of every (head, query block).  The score of key block j is
+ * <q_mean, k_mean[j]> / sqrt(D), formed in 64 bits from the fp32 means (their
+ * products are exact), so a list does not depend on the machine's order of
+ * work.  A list holds the keep_first first and keep_last last blocks, then
+ * the blocks of highest score, the lower index first among equal ones, up to
+ * topk in all; of these, blocks that are not kept by position and score less
+ * than the row's highest score - margin are dropped.  NaN scores count as
+ * -infinity.
+ *   q_mean  fp32 [H][nq][D], k_mean fp32 [Hkv][nk][D] (device, read)
+ *   idx     int32 [H][nq][topk] (device, written): the list in increasing
+ *           order, then -1
+ *   count   int32 [H][nq] (device, written): entries of each list
+ * One launch.  H, nq or nk = 0: nothing to select; nk = 0 writes empty lists.
+ * Errors: DT_ERR_INVALID, DT_ERR_UNSUPPORTED (misaligned pointer, nk over the
+ * limit), DT_ERR_CUDA. */
+DT_API int dt_block_select(const dt_select_params* p, const float* q_mean, const float* k_mean,
+                    int32_t* idx, int32_t* count, void* stream);
+
+typedef struct {
+  int32_t H, Hkv;               /* query heads; key heads: query head h reads key head h / (H/Hkv) */
+  int32_t Sq, Sk;               /* query rows, key rows */
+  int32_t D;                    /* 64, 72 or 128 */
+  int32_t k_block;              /* key rows per block: 64 or 128 */
+  int32_t cap;                  /* entries allocated per list */
+  int32_t type;                 /* of Q, K, V: DT_TYPE_BF16 or DT_TYPE_F16 */
+  int32_t out_type;             /* of O: type, or DT_TYPE_F32 (OUT as dt_state_merge reads it) */
+  dt_strides q, k, v, o;
+} dt_sparse_params;
+
+/* Attention of every query block (DT_TILE = 128 rows; the last may be short)
+ * over the key blocks of its list: for query row s of head h, over the keys of
+ * blocks idx[h][s/128][0 .. count-1] (block j = rows [j*k_block, min((j+1)*
+ * k_block, Sk))): OUT = softmax(q K^T / sqrt(D)) V and its natural-log LSE, a
+ * state that composes with any other.  A row with an empty list gets (0,
+ * -inf).  A block listed twice counts twice; any order is allowed.
+ *   Q, O     [H][Sq][D], K, V [Hkv][Sk][D], strides p->q, p->o, p->k, p->v
+ *   idx      int32 [H][ceil(Sq/128)][cap] (device, read)
+ *   count    int32 [H][ceil(Sq/128)] (device, read), or NULL: cap entries each
+ *   L        fp32 [H][Sq] (written)
+ *   d_status int32 device status word (see conventions).  A count outside
+ *            [0, cap] is clamped and an entry outside [0, ceil(Sk/k_block))
+ *            contributes nothing; both write DT_ERR_INVALID to it
+ * Row starts must be 16-byte aligned (pointers and strides); strides > 0, and
+ * those of Q, K and V below 2^40 bytes.
+ * With few query blocks the CTAs of a cluster split each list and join their
+ * states through distributed shared memory: one launch, no workspace, and the
+ * same result run to run.  Sq = 0 or H = 0 launches nothing.  Errors:
+ * DT_ERR_INVALID, DT_ERR_UNSUPPORTED (D, types, alignment), DT_ERR_CUDA;
+ * DT_ERR_TIMEOUT and DT_ERR_INVALID through d_status. */
+DT_API int dt_attn_block_sparse(const dt_sparse_params* p, const void* Q, const void* K, const void* V,
+                         const int32_t* idx, const int32_t* count, void* O, float* L,
+                         int32_t* d_status, void* stream);
+
+/* Limit, in nanoseconds, of every bounded wait inside the attention kernels
  * (default 2e9).  A wait that runs out writes DT_ERR_TIMEOUT to *d_status and
  * the kernel drains its in-flight copies, frees its tensor memory and
  * returns.  Process-wide setting used by later launches.  Returns DT_OK. */

@@ -28,7 +28,10 @@ __all__ = [
     "dt_plan_build_importance", "dt_state_importance", "dt_share_output", "dt_key_set_tiles",
     "dt_attn_cfg_shared", "dt_plan_share_counts", "DT_SHARE_CFG", "DT_SHARE_TIMESTEP",
     "DT_MODE_ANCHOR", "AnchorState", "dt_anchor_init", "dt_plan_build_anchor", "dt_anchor_update",
-    "dt_attn_partial_fused_tracked",
+    "dt_attn_partial_fused_tracked", "DT_TYPE_BF16", "DT_TYPE_F16", "DT_TYPE_F32", "DT_ROPE_INTERLEAVED",
+    "DT_ROPE_HALVES", "Strides", "RopeParams", "NormRopeParams", "SelectParams", "SparseParams", "rope_params",
+    "norm_rope_params", "select_params", "sparse_params", "dt_rope_table", "dt_qk_norm_rope", "dt_block_select",
+    "dt_attn_block_sparse",
 ]
 
 DT_OK, DT_ERR_INVALID, DT_ERR_UNSUPPORTED, DT_ERR_CACHE_EMPTY, DT_ERR_CUDA, DT_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
@@ -40,6 +43,9 @@ DT_PLAN_REUSE, DT_PLAN_COMPUTE = 0, 1
 DT_WR_MAKE, DT_WR_APPLY = 0, 1
 DT_SHARE_CFG, DT_SHARE_TIMESTEP = 0, 1
 DT_TILE = 128
+DT_TYPE_BF16, DT_TYPE_F16, DT_TYPE_F32 = 0, 1, 2
+DT_ROPE_INTERLEAVED, DT_ROPE_HALVES = 0, 1
+DT_ROPE_MAX_AXES = 4
 
 
 class DtError(RuntimeError):
@@ -66,6 +72,32 @@ class AnchorState(ctypes.Structure):
     _fields_ = [("weights", ctypes.POINTER(ctypes.c_float)), ("alpha", ctypes.POINTER(ctypes.c_float)),
                 ("drift", ctypes.POINTER(ctypes.c_float)), ("eps", ctypes.c_float), ("theta", ctypes.c_float),
                 ("target_ratio", ctypes.c_float), ("last_anchor", ctypes.c_int32), ("anchored", ctypes.c_int32)]
+
+
+class Strides(ctypes.Structure):
+    """dt_strides: element strides of the heads and rows of a [head][row][D] tensor."""
+    _fields_ = [("head", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [("S", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("dim", ctypes.c_int32 * DT_ROPE_MAX_AXES),
+                ("base", ctypes.c_double)]
+
+
+class NormRopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("S", "D", "H", "Hkv", "rot", "pairing", "in_type", "out_type", "norm",
+                                              "q_block", "k_block")] + [("eps", ctypes.c_float)] + \
+               [(n, Strides) for n in ("q_in", "k_in", "v_in", "q_out", "k_out", "v_out")]
+
+
+class SelectParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("H", "Hkv", "nq", "nk", "D", "topk", "keep_first", "keep_last")] + \
+               [("margin", ctypes.c_double)]
+
+
+class SparseParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("H", "Hkv", "Sq", "Sk", "D", "k_block", "cap", "type", "out_type")] + \
+               [(n, Strides) for n in ("q", "k", "v", "o")]
 
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -106,6 +138,10 @@ def load() -> ctypes.CDLL:
             "dt_anchor_update": ([pp, ctypes.POINTER(AnchorState), vp, vp, vp, vp], ctypes.c_int),
             "dt_attn_partial_fused_tracked": ([pp] + [vp] * 11 + [i32, vp], ctypes.c_int),
             "dt_key_set_tiles": ([pp, i32, i32, vp, vp, i32], ctypes.c_int),
+            "dt_rope_table": ([ctypes.POINTER(RopeParams), vp, vp, vp], ctypes.c_int),
+            "dt_qk_norm_rope": ([ctypes.POINTER(NormRopeParams)] + [vp] * 12, ctypes.c_int),
+            "dt_block_select": ([ctypes.POINTER(SelectParams)] + [vp] * 5, ctypes.c_int),
+            "dt_attn_block_sparse": ([ctypes.POINTER(SparseParams)] + [vp] * 9, ctypes.c_int),
             "dt_set_wait_limit_ns": ([i64], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -330,6 +366,169 @@ def dt_state_cache_update(p: PlanParams, d_plan, fresh_O, fresh_L, cache_O, cach
 def dt_window_residual(op, H, S, D, O_full, O_win, R, O, d_status=None, stream=None) -> None:
     _check(load().dt_window_residual(op, H, S, D, _ptr(O_full), _ptr(O_win), _ptr(R), _ptr(O), _ptr(d_status),
                                      _stream(stream)), "dt_window_residual")
+
+
+# ---- block-sparse attention and the passes in front of it -------------------
+# These take torch tensors, check them against the parameters (a wrong size
+# would be read or written out of bounds on the device) and run on the tensors'
+# device: on `stream` where given, else on that device's current stream.
+
+def _type_of(t) -> int:
+    import torch
+    try:
+        return {torch.bfloat16: DT_TYPE_BF16, torch.float16: DT_TYPE_F16, torch.float32: DT_TYPE_F32}[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported element type {t.dtype}") from None
+
+
+def _heads(t, name: str) -> "Strides":
+    """Strides of a [heads][rows][D] tensor or view whose rows are contiguous."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: expected [heads][rows][D] with contiguous rows, got {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    return Strides(t.stride(0), t.stride(1))
+
+
+def _match(t, shape, dtype, name: str, like=None) -> None:
+    """Raise unless t is a contiguous tensor of this shape and type (on like's device)."""
+    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)} "
+                         f"with strides {t.stride()}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
+
+
+def _match_heads(t, shape, strides, ty: int, name: str, like=None) -> None:
+    """Raise unless t is the [heads][rows][D] tensor that the parameters were made for."""
+    if tuple(t.shape) != shape or _type_of(t) != ty or (t.shape[2] > 1 and t.stride(2) != 1) or \
+            (shape[0] > 1 and t.stride(0) != strides.head) or (shape[1] > 1 and t.stride(1) != strides.row):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} is not what the parameters "
+                         f"describe: {shape}, head stride {strides.head}, row stride {strides.row}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
+
+
+def _call(name: str, like, stream, p, *args) -> None:
+    """One C call with like's device current (launches go to the current device)."""
+    import torch
+    if not like.is_cuda:
+        raise ValueError(f"{name}: expected CUDA tensors, got one on {like.device}")
+    f = getattr(load(), name)
+    if like.device.index == torch.cuda.current_device():
+        status = f(ctypes.byref(p), *args, _stream(stream))
+    else:
+        with torch.cuda.device(like.device):
+            status = f(ctypes.byref(p), *args, _stream(stream))
+    _check(status, name)
+
+
+def rope_params(S: int, axes, base: float = 10000.0) -> RopeParams:
+    """Rotation of S tokens over position axes; axes: rotated dimensions of each."""
+    axes = list(axes)
+    if not 1 <= len(axes) <= DT_ROPE_MAX_AXES:
+        raise ValueError(f"1 to {DT_ROPE_MAX_AXES} axes, got {len(axes)}")
+    return RopeParams(S, len(axes), (ctypes.c_int32 * DT_ROPE_MAX_AXES)(*axes), base)
+
+
+def dt_rope_table(p: RopeParams, pos, table, stream=None) -> None:
+    """pos: int32 [axes][S]; table: float32 [S][rot/2][2], written with (cos, sin)."""
+    import torch
+    _match(pos, (p.n_axes, p.S), torch.int32, "pos")
+    _match(table, (p.S, sum(p.dim[:p.n_axes]) // 2, 2), torch.float32, "table", pos)
+    _call("dt_rope_table", pos, stream, p, _ptr(pos), _ptr(table))
+
+
+def norm_rope_params(q=None, k=None, v=None, Q=None, K=None, V=None, rot: int = 0,
+                     pairing: int = DT_ROPE_INTERLEAVED, norm: bool = True, eps: float = 1e-6, q_block: int = DT_TILE,
+                     k_block: int = 64) -> NormRopeParams:
+    """Parameters of dt_qk_norm_rope for tensors (or views) laid out like these:
+    q [H][S][D], k and v [Hkv][S][D] inputs, Q, K, V outputs; a part may be
+    None.  x.view(S, heads, D).transpose(0, 1) is a token-major projection."""
+    ins, outs = [t for t in (q, k, v) if t is not None], [t for t in (Q, K, V) if t is not None]
+    if not ins:
+        raise ValueError("no input")
+    S, D = ins[0].shape[1], ins[0].shape[2]
+    ity = _type_of(ins[0])
+    p = NormRopeParams(S=S, D=D, H=0 if q is None else q.shape[0],
+                       Hkv=0 if k is None and v is None else (k if k is not None else v).shape[0], rot=rot,
+                       pairing=pairing, in_type=ity, out_type=_type_of(outs[0]) if outs else ity, norm=int(norm),
+                       q_block=q_block, k_block=k_block, eps=eps)
+    for n, t in (("q_in", q), ("k_in", k), ("v_in", v), ("q_out", Q), ("k_out", K), ("v_out", V)):
+        if t is not None:
+            setattr(p, n, _heads(t, n))
+    return p
+
+
+def dt_qk_norm_rope(p: NormRopeParams, q, k, v, wq, wk, table, Q, K, V, q_mean=None, k_mean=None, stream=None) -> None:
+    """Per-head RMS norm, rotation, layout change and block means in one pass
+    (see norm_rope_params).  wq, wk: float32 [D] or None; table: dt_rope_table's,
+    None with rot = 0; q_mean, k_mean: float32 [heads][blocks][D] or None."""
+    import torch
+    like = next((t for t in (q, k, v) if t is not None), None)
+    if like is None:
+        raise ValueError("no input")
+    for t, n, heads, ty in ((q, "q_in", p.H, p.in_type), (k, "k_in", p.Hkv, p.in_type), (v, "v_in", p.Hkv, p.in_type),
+                            (Q, "q_out", p.H, p.out_type), (K, "k_out", p.Hkv, p.out_type),
+                            (V, "v_out", p.Hkv, p.out_type)):
+        if t is not None:
+            _match_heads(t, (heads, p.S, p.D), getattr(p, n), ty, n, like)
+    for t, n in ((wq, "wq"), (wk, "wk")):
+        if t is not None:
+            _match(t, (p.D,), torch.float32, n, like)
+    if p.rot and table is not None:
+        _match(table, (p.S, p.rot // 2, 2), torch.float32, "table", like)
+    for t, n, heads, block in ((q_mean, "q_mean", p.H, p.q_block), (k_mean, "k_mean", p.Hkv, p.k_block)):
+        if t is not None and block > 0:
+            _match(t, (heads, -(-p.S // block), p.D), torch.float32, n, like)
+    _call("dt_qk_norm_rope", like, stream, p, _ptr(q), _ptr(k), _ptr(v), _ptr(wq), _ptr(wk), _ptr(table), _ptr(Q),
+          _ptr(K), _ptr(V), _ptr(q_mean), _ptr(k_mean))
+
+
+def select_params(H: int, Hkv: int, nq: int, nk: int, D: int, topk: int, keep_first: int = 0, keep_last: int = 0,
+                  margin: float = float("inf")) -> SelectParams:
+    return SelectParams(H, Hkv, nq, nk, D, topk, keep_first, keep_last, margin)
+
+
+def dt_block_select(p: SelectParams, q_mean, k_mean, idx, count, stream=None) -> None:
+    """Lists of key blocks by the scores of block means.  q_mean float32
+    [H][nq][D], k_mean float32 [Hkv][nk][D]; idx int32 [H][nq][topk] and count
+    int32 [H][nq] are written."""
+    import torch
+    _match(q_mean, (p.H, p.nq, p.D), torch.float32, "q_mean")
+    _match(k_mean, (p.Hkv, p.nk, p.D), torch.float32, "k_mean", q_mean)
+    _match(idx, (p.H, p.nq, p.topk), torch.int32, "idx", q_mean)
+    _match(count, (p.H, p.nq), torch.int32, "count", q_mean)
+    _call("dt_block_select", q_mean, stream, p, _ptr(q_mean), _ptr(k_mean), _ptr(idx), _ptr(count))
+
+
+def sparse_params(Q, K, V, O, k_block: int = 64, cap: int = 0) -> SparseParams:
+    """Parameters of dt_attn_block_sparse for tensors (or views) laid out like
+    these: Q, O [H][Sq][D], K, V [Hkv][Sk][D]; cap entries per list."""
+    p = SparseParams(H=Q.shape[0], Hkv=K.shape[0], Sq=Q.shape[1], Sk=K.shape[1], D=Q.shape[2], k_block=k_block,
+                     cap=cap, type=_type_of(Q), out_type=_type_of(O))
+    for n, t in (("q", Q), ("k", K), ("v", V), ("o", O)):
+        setattr(p, n, _heads(t, n))
+    return p
+
+
+def dt_attn_block_sparse(p: SparseParams, Q, K, V, idx, count, O, L, d_status, stream=None) -> None:
+    """Attention of every 128-row query block over the key blocks of its list:
+    the state (O, L).  idx int32 [H][ceil(Sq/128)][cap], count int32
+    [H][ceil(Sq/128)] or None (cap entries each), L float32 [H][Sq], d_status
+    int32 device status word."""
+    import torch
+    for t, n, shape, ty in ((Q, "q", (p.H, p.Sq, p.D), p.type), (K, "k", (p.Hkv, p.Sk, p.D), p.type),
+                            (V, "v", (p.Hkv, p.Sk, p.D), p.type), (O, "o", (p.H, p.Sq, p.D), p.out_type)):
+        _match_heads(t, shape, getattr(p, n), ty, n.upper(), Q)
+    nqb = -(-p.Sq // DT_TILE)
+    _match(idx, (p.H, nqb, p.cap), torch.int32, "idx", Q)
+    if count is not None:
+        _match(count, (p.H, nqb), torch.int32, "count", Q)
+    _match(L, (p.H, p.Sq), torch.float32, "L", Q)
+    if d_status.dtype != torch.int32 or d_status.numel() < 1 or d_status.device != Q.device:
+        raise ValueError("d_status: expected an int32 tensor on the inputs' device")
+    _call("dt_attn_block_sparse", Q, stream, p, _ptr(Q), _ptr(K), _ptr(V), _ptr(idx), _ptr(count), _ptr(O), _ptr(L),
+          _ptr(d_status))
 
 
 def dt_set_wait_limit_ns(ns: int) -> None:

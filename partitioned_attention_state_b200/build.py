@@ -15,19 +15,24 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdt.so")
-SOURCES = ["plan.cpp", "api.cu", "attn_fused_sm100.cu", "state_ops.cu"]
+SOURCES = ["plan.cpp", "api.cu", "attn_fused_sm100.cu", "attn_sparse_sm100.cu", "state_ops.cu", "token_ops.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr"]
 
 
-def _check_launch_registers(ptxas_log: str) -> None:
-    """The fused kernel splits its launch register pool between warpgroups
+# kernels that split their launch registers between warpgroups: source -> entry name
+SPLIT_KERNELS = {"attn_fused_sm100.cu": "attn_partial_fused_kernel",
+                 "attn_sparse_sm100.cu": "attn_block_sparse_kernel"}
+
+
+def _check_launch_registers(source: str, ptxas_log: str) -> None:
+    """The attention kernels split their launch register pool between warpgroups
     with setmaxnreg; the split is sized for exactly kLaunchRegs registers per
     thread at launch.  A smaller pool would make setmaxnreg.inc wait forever,
     so refuse to build if ptxas chose another count."""
-    src = open(os.path.join(CSRC, "attn_fused_sm100.cu")).read()
+    src = open(os.path.join(CSRC, source)).read()
     want = int(re.search(r"constexpr int kLaunchRegs = (\d+);", src).group(1))
     found = []
     cur = None
@@ -36,10 +41,10 @@ def _check_launch_registers(ptxas_log: str) -> None:
         if m:
             cur = m.group(1)
         m = re.search(r"Used (\d+) registers", line)
-        if m and cur and "attn_partial_fused_kernel" in cur:
+        if m and cur and SPLIT_KERNELS[source] in cur:
             found.append(int(m.group(1)))
     if not found or any(n != want for n in found):
-        raise RuntimeError(f"fused kernel launch registers {found} != {want}: setmaxnreg split would not fit")
+        raise RuntimeError(f"{source}: launch registers {found} != {want}: setmaxnreg split would not fit")
 
 
 def _newer(out: str, deps) -> bool:
@@ -65,8 +70,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
         res = subprocess.run(cmd, check=True, capture_output=True, text=True)
         if verbose:
             sys.stderr.write(res.stderr)
-        if src == "attn_fused_sm100.cu":
-            _check_launch_registers(res.stderr)
+        if src in SPLIT_KERNELS:
+            _check_launch_registers(src, res.stderr)
         objs.append(obj)
     cmd = [NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", LIB + ".tmp", *objs]
     if verbose:

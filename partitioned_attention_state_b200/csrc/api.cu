@@ -6,12 +6,15 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "../../include/dt.h"
 #include "attn_fused.h"
+#include "attn_sparse.h"
 #include "geometry.h"
 #include "state_ops.h"
+#include "token_ops.h"
 
 namespace {
 
@@ -313,4 +316,189 @@ extern "C" int dt_window_residual(int32_t op, int32_t H, int32_t S, int32_t D, c
   int sms = 0;
   if (int e = sm_count(&sms)) return e;
   return dt::launch_window_residual(op, n, O_full, O_win, R, O, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---- block-sparse attention and the passes in front of it -------------------
+namespace {
+
+int type_size(int t) { return t == DT_TYPE_F32 ? 4 : 2; }
+bool type_ok(int t) { return t == DT_TYPE_BF16 || t == DT_TYPE_F16 || t == DT_TYPE_F32; }
+// rows that start on 16-byte boundaries: strides of n > 1 heads / rows must be
+// multiples of 16 bytes (a stride that no element uses is not looked at)
+bool strides_aligned(const dt_strides& s, int heads, int rows, int size) {
+  return (heads <= 1 || s.head * size % 16 == 0) && (rows <= 1 || s.row * size % 16 == 0);
+}
+bool strides_nonneg(const dt_strides& s, int heads, int rows) {
+  return (heads <= 1 || s.head >= 0) && (rows <= 1 || s.row >= 0);
+}
+
+// 16-bit [heads][S][D] with element strides as a 3-D tensor (D, S, heads); box (bw, 64, 1)
+bool encode_strided(CUtensorMap* m, const void* base, int heads, int S, int D, dt_strides st, bool f16, int bw,
+                    CUtensorMapSwizzle sw) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)S, (cuuint64_t)heads};
+  // an extent of 1 never uses its stride: any legal one will do
+  const cuuint64_t row = S > 1 ? (cuuint64_t)st.row * 2 : (cuuint64_t)((D * 2 + 15) / 16 * 16);
+  const cuuint64_t head = heads > 1 ? (cuuint64_t)st.head * 2 : row;
+  cuuint64_t strides[2] = {row, head};
+  cuuint32_t box[3] = {(cuuint32_t)bw, 64u, 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" int dt_rope_table(const dt_rope_params* p, const int32_t* pos, float* table, void* stream) {
+  if (!p || p->S < 0 || p->n_axes < 1 || p->n_axes > DT_ROPE_MAX_AXES) return DT_ERR_INVALID;
+  if (!(p->base > 0.0) || !std::isfinite(p->base)) return DT_ERR_INVALID;
+  int64_t rot = 0;
+  for (int a = 0; a < p->n_axes; ++a) {
+    if (p->dim[a] < 2 || p->dim[a] % 2 != 0) return DT_ERR_INVALID;
+    rot += p->dim[a];
+  }
+  if (rot > 2 * dt::kMaxPairs) return DT_ERR_INVALID;
+  if (p->S == 0) return DT_OK;
+  if (!pos || !table) return DT_ERR_INVALID;
+  if (!aligned16(pos) || !aligned16(table)) return DT_ERR_UNSUPPORTED;
+  dt::RopeTableArgs a;
+  memset(&a, 0, sizeof(a));
+  a.pos = pos;
+  a.table = table;
+  a.S = p->S;
+  for (int x = 0; x < p->n_axes; ++x)
+    for (int j = 0; j < p->dim[x] / 2; ++j) {
+      a.turns[a.pairs] = pow(p->base, -2.0 * j / p->dim[x]) / 6.283185307179586476925;
+      a.axis[a.pairs++] = (uint8_t)x;
+    }
+  return dt::launch_rope_table(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dt_qk_norm_rope(const dt_norm_rope_params* p, const void* q, const void* k, const void* v,
+                               const float* wq, const float* wk, const float* table, void* Q, void* K, void* V,
+                               float* q_mean, float* k_mean, void* stream) {
+  if (!p || p->S < 0 || p->S > 1 << 30 || p->D < 8 || p->D > 128 || p->D % 8 != 0) return DT_ERR_INVALID;
+  if (p->H < 0 || p->Hkv < 0 || p->H > 1 << 14 || p->Hkv > 1 << 14) return DT_ERR_INVALID;
+  if (p->rot < 0 || p->rot > p->D || p->rot % 8 != 0) return DT_ERR_INVALID;
+  if (p->pairing != DT_ROPE_INTERLEAVED && p->pairing != DT_ROPE_HALVES) return DT_ERR_INVALID;
+  if (!type_ok(p->in_type) || !type_ok(p->out_type)) return DT_ERR_INVALID;
+  if (p->out_type != p->in_type && p->out_type != DT_TYPE_BF16) return DT_ERR_UNSUPPORTED;
+  if (p->norm != 0 && p->norm != 1) return DT_ERR_INVALID;
+  if (p->norm && !(p->eps >= 0.f && p->eps < INFINITY)) return DT_ERR_INVALID;
+  if ((q_mean && p->q_block != 64 && p->q_block != 128) || (k_mean && p->k_block != 64 && p->k_block != 128))
+    return DT_ERR_INVALID;
+  // a part without an input has no outputs; a part with one has something to write
+  if (q ? (!Q && !q_mean) : (Q || q_mean)) return DT_ERR_INVALID;
+  if (k ? (!K && !k_mean) : (K || k_mean)) return DT_ERR_INVALID;
+  if ((v != nullptr) != (V != nullptr)) return DT_ERR_INVALID;
+  if (p->rot > 0 && (q || k) && !table && p->S > 0) return DT_ERR_INVALID;
+  struct { const void* p; dt_strides s; int heads, size; } t[] = {
+      {q, p->q_in, p->H, type_size(p->in_type)},    {k, p->k_in, p->Hkv, type_size(p->in_type)},
+      {v, p->v_in, p->Hkv, type_size(p->in_type)},  {Q, p->q_out, p->H, type_size(p->out_type)},
+      {K, p->k_out, p->Hkv, type_size(p->out_type)}, {V, p->v_out, p->Hkv, type_size(p->out_type)}};
+  for (const auto& x : t)
+    if (x.p) {
+      if (!strides_nonneg(x.s, x.heads, p->S)) return DT_ERR_INVALID;
+      if (!aligned16(x.p) || !strides_aligned(x.s, x.heads, p->S, x.size)) return DT_ERR_UNSUPPORTED;
+    }
+  for (const void* x : {(const void*)wq, (const void*)wk, (const void*)table, (const void*)q_mean, (const void*)k_mean})
+    if (x && !aligned16(x)) return DT_ERR_UNSUPPORTED;
+  if (p->S == 0 || p->H + p->Hkv == 0) return DT_OK;
+  if (!q && !k && !v) return DT_OK;
+  int sms = 0;
+  if (int e = sm_count(&sms)) return e;
+  dt::NormRopeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.q = q; a.k = k; a.v = v;
+  a.Q = Q; a.K = K; a.V = V;
+  a.wq = wq; a.wk = wk; a.table = table;
+  a.q_mean = q_mean; a.k_mean = k_mean;
+  a.p = *p;
+  return dt::launch_qk_norm_rope(a, sms, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dt_block_select(const dt_select_params* p, const float* q_mean, const float* k_mean, int32_t* idx,
+                               int32_t* count, void* stream) {
+  if (!p || p->H < 0 || p->nq < 0 || p->nk < 0) return DT_ERR_INVALID;
+  if (p->D < 4 || p->D > 128 || p->D % 4 != 0 || p->topk < 1) return DT_ERR_INVALID;
+  if (p->keep_first < 0 || p->keep_last < 0 || (int64_t)p->keep_first + p->keep_last > p->topk) return DT_ERR_INVALID;
+  if (!(p->margin >= 0.0)) return DT_ERR_INVALID;
+  if (p->H > 0 && (p->Hkv < 1 || p->H % p->Hkv != 0)) return DT_ERR_INVALID;
+  if ((int64_t)p->H * p->nq >= (int64_t)1 << 31) return DT_ERR_INVALID;
+  if (p->nk > DT_SELECT_MAX_BLOCKS) return DT_ERR_UNSUPPORTED;
+  if (p->H == 0 || p->nq == 0) return DT_OK;
+  if (!q_mean || (!k_mean && p->nk > 0) || !idx || !count) return DT_ERR_INVALID;
+  if (!aligned16(q_mean) || !aligned16(k_mean) || !aligned16(idx) || !aligned16(count)) return DT_ERR_UNSUPPORTED;
+  return dt::launch_block_select(*p, q_mean, k_mean, idx, count, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int dt_attn_block_sparse(const dt_sparse_params* p, const void* Q, const void* K, const void* V,
+                                    const int32_t* idx, const int32_t* count, void* O, float* L, int32_t* d_status,
+                                    void* stream) {
+  if (!p || p->H < 0 || p->Sq < 0 || p->Sk < 0 || p->cap < 0) return DT_ERR_INVALID;
+  if (p->H > 0 && (p->Hkv < 1 || p->H % p->Hkv != 0)) return DT_ERR_INVALID;
+  if (p->k_block != 64 && p->k_block != 128) return DT_ERR_INVALID;
+  if (!type_ok(p->type) || !type_ok(p->out_type)) return DT_ERR_INVALID;
+  if (p->type == DT_TYPE_F32 || (p->out_type != p->type && p->out_type != DT_TYPE_F32)) return DT_ERR_UNSUPPORTED;
+  if (p->D != 64 && p->D != 72 && p->D != 128) return DT_ERR_UNSUPPORTED;
+  if (p->Sq > 1 << 30 || p->Sk > 1 << 30) return DT_ERR_INVALID;
+  const int nqb = dt::ceil_div(p->Sq, DT_TILE);
+  if ((int64_t)p->H * nqb * 16 >= (int64_t)1 << 31) return DT_ERR_INVALID;
+  if (p->H == 0 || p->Sq == 0) return DT_OK;
+  if (!Q || !O || !L || !d_status || (p->Sk > 0 && (!K || !V)) || (p->cap > 0 && !idx)) return DT_ERR_INVALID;
+  if (p->Sk == 0 && p->cap > 0 && !count) return DT_ERR_INVALID;       // lists of nothing but bad entries
+  const int osize = type_size(p->out_type);
+  const struct { const void* p; dt_strides s; int heads, rows, size; } t[] = {{Q, p->q, p->H, p->Sq, 2},
+                                                                             {K, p->k, p->Hkv, p->Sk, 2},
+                                                                             {V, p->v, p->Hkv, p->Sk, 2},
+                                                                             {O, p->o, p->H, p->Sq, osize}};
+  for (const auto& x : t) {
+    if ((x.heads > 1 && (x.s.head <= 0 || x.s.head >= (int64_t)1 << 39)) ||
+        (x.rows > 1 && (x.s.row <= 0 || x.s.row >= (int64_t)1 << 39)))
+      return DT_ERR_INVALID;
+    if (!aligned16(x.p) || !strides_aligned(x.s, x.heads, x.rows, x.size)) return DT_ERR_UNSUPPORTED;
+  }
+  if (!aligned16(idx) || !aligned16(count) || !aligned16(L) || !aligned16(d_status)) return DT_ERR_UNSUPPORTED;
+
+  dt::SparseParams kp;
+  memset(&kp, 0, sizeof(kp));
+  const bool f16 = p->type == DT_TYPE_F16;
+  const CUtensorMapSwizzle sw128 = CU_TENSOR_MAP_SWIZZLE_128B, sw32 = CU_TENSOR_MAP_SWIZZLE_32B;
+  // no keys: every list counts as empty (cap 0 below), so no box is ever
+  // loaded from K and V and their maps may stand on Q's memory
+  const bool keys = p->Sk > 0;
+  const void* Kb = keys ? K : Q;
+  const void* Vb = keys ? V : Q;
+  const int kr = keys ? p->Sk : 1, kh = keys ? p->Hkv : 1;
+  bool ok = encode_strided(&kp.tmQ, Q, p->H, p->Sq, p->D, p->q, f16, 64, sw128) &&
+            encode_strided(&kp.tmK, Kb, kh, kr, p->D, p->k, f16, 64, sw128) &&
+            encode_strided(&kp.tmV, Vb, kh, kr, p->D, p->v, f16, 64, sw128);
+  if (ok && p->D == 72)
+    ok = encode_strided(&kp.tmQt, Q, p->H, p->Sq, p->D, p->q, f16, 16, sw32) &&
+         encode_strided(&kp.tmKt, Kb, kh, kr, p->D, p->k, f16, 16, sw32) &&
+         encode_strided(&kp.tmVt, Vb, kh, kr, p->D, p->v, f16, 16, sw32);
+  if (!ok) return DT_ERR_CUDA;
+  kp.idx = idx;
+  kp.count = count;
+  kp.O = O;
+  kp.L = L;
+  kp.status = d_status;
+  kp.o_head = p->o.head;
+  kp.o_row = p->o.row;
+  kp.H = p->H;
+  kp.per_kv = p->H / p->Hkv;
+  kp.Sq = p->Sq;
+  kp.Sk = p->Sk;
+  kp.nqb = nqb;
+  kp.nkb = dt::ceil_div(p->Sk, p->k_block);
+  kp.cap = keys ? p->cap : 0;
+  kp.per_tile = DT_TILE / p->k_block;
+  kp.out_f32 = p->out_type == DT_TYPE_F32;
+  kp.scale_log2 = (float)(1.4426950408889634 / sqrt((double)p->D));
+  kp.wait_limit_ns = (uint64_t)g_wait_limit_ns.load();
+  int sms = 0;
+  if (int e = sm_count(&sms)) return e;
+  return dt::launch_attn_sparse(kp, p->D == 72 ? 80 : p->D, f16, sms, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -9,7 +9,9 @@ copies.  The key sets are partitions or groups of partitions (``group``),
 the cached OUT fp32 or bf16 (``state_dtype``); plans follow the proximity
 rule, an explicit plan, or measured importance (``measure_importance``);
 cached group states can be regrouped (``compose_groups``) and outputs shared
-across CFG branches or timesteps.  torch provides the memory and the
+across CFG branches or timesteps.  The inputs can come straight from a layer's
+projections (``set_projection``), and a step can attend only the key blocks that
+block means select (``step_sparse``).  torch provides the memory and the
 streams; every computation happens in libdt.
 """
 
@@ -20,11 +22,12 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (DT_MODE_ANCHOR, DT_MODE_IMPORTANCE, DT_MODE_PROXIMITY, DT_MODE_WINDOW, DT_SHARE_CFG,
-               DT_SHARE_TIMESTEP, dt_anchor_update, dt_attn_cfg_shared, dt_attn_partial_fused,
-               dt_attn_partial_fused_heads, dt_attn_partial_fused_tracked, dt_group_compose, dt_plan_build,
-               dt_plan_build_anchor, dt_plan_build_importance, dt_plan_geometry, dt_plan_share_counts,
-               dt_state_importance, new_anchor_state, DtError, params)
+from . import (DT_MODE_ANCHOR, DT_MODE_IMPORTANCE, DT_MODE_PROXIMITY, DT_MODE_WINDOW, DT_ROPE_INTERLEAVED,
+               DT_SHARE_CFG, DT_SHARE_TIMESTEP, DT_TILE, dt_anchor_update, dt_attn_block_sparse, dt_attn_cfg_shared,
+               dt_attn_partial_fused, dt_attn_partial_fused_heads, dt_attn_partial_fused_tracked, dt_block_select,
+               dt_group_compose, dt_plan_build, dt_plan_build_anchor, dt_plan_build_importance, dt_plan_geometry,
+               dt_plan_share_counts, dt_qk_norm_rope, dt_state_importance, new_anchor_state, norm_rope_params,
+               select_params, sparse_params, DtError, params)
 
 
 def bf16_from_bits(bits: np.ndarray, device) -> torch.Tensor:
@@ -85,6 +88,8 @@ class Session:
             self.last_anchored = False
         self.last_counts = None
         self.last_plan = None
+        self.q_mean = self.k_mean = None      # block means of the last set_projection or step_sparse
+        self.lists = None                     # (idx, count) of the last step_sparse
 
     def _plan_buffers(self) -> None:
         self.d_plan = torch.zeros((max(self.nqt, 1), self.nseg), dtype=torch.uint8, device=self.device)
@@ -123,6 +128,28 @@ class Session:
                 dst.copy_(bf16_from_bits(src, "cpu"))
             else:
                 dst.copy_(src)
+
+    def _means(self, k_block: int) -> None:
+        nq, nk = -(-self.S // DT_TILE), -(-self.S // k_block)
+        if self.k_mean is None or self.k_mean.shape[1] != nk:
+            self.q_mean = torch.empty((self.H, nq, self.D), dtype=torch.float32, device=self.device)
+            self.k_mean = torch.empty((self.H, nk, self.D), dtype=torch.float32, device=self.device)
+
+    def set_projection(self, qkv: torch.Tensor, wq=None, wk=None, table=None, pairing: int = DT_ROPE_INTERLEAVED,
+                       norm: bool = True, eps: float = 1e-6, k_block: int = 64, stream=None) -> None:
+        """Inputs from the layer's packed projection (dt_qk_norm_rope): qkv
+        [S][3*H*D] (queries, keys, values, each [H][D]; bf16, fp16 or fp32) on
+        the session's device is normalised per head (weights wq, wk float32
+        [D]), rotated by the tokens' table (dt_rope_table; None: not rotated)
+        and written to Q, K and V, in one pass that also leaves the block means
+        of Q (DT_TILE rows) and K (k_block rows) for step_sparse."""
+        if tuple(qkv.shape) != (self.S, 3 * self.H * self.D):
+            raise ValueError(f"qkv: expected {(self.S, 3 * self.H * self.D)}, got {tuple(qkv.shape)}")
+        x = qkv.unflatten(1, (3, self.H, self.D)).permute(1, 2, 0, 3)
+        self._means(k_block)
+        p = norm_rope_params(x[0], x[1], x[2], self.Q, self.K, self.V, rot=0 if table is None else 2 * table.shape[1],
+                             pairing=pairing, norm=norm, eps=eps, q_block=DT_TILE, k_block=k_block)
+        dt_qk_norm_rope(p, x[0], x[1], x[2], wq, wk, table, self.Q, self.K, self.V, self.q_mean, self.k_mean, stream)
 
     # -------------------------------------------------------------- planning
     def plan(self, step: int, mode: Optional[int] = None, explicit: Optional[np.ndarray] = None):
@@ -209,6 +236,32 @@ class Session:
             ev = torch.cuda.Event()
             ev.record(st)
         self._uploaded[i] = ev
+
+    def step_sparse(self, topk: int, keep_first: int = 0, keep_last: int = 0, margin: float = float("inf"),
+                    k_block: int = 64, remeasure: bool = True, stream=None) -> None:
+        """One sparse step into O and L: every 128-row query block attends the
+        topk key blocks of k_block rows that dt_block_select chooses for it
+        (keep_first, keep_last, margin: see there).  The state cache, the
+        stamps and the plan are left alone.  remeasure=False takes the block
+        means that set_projection (same k_block) left, which is right as long as
+        Q and K are what it wrote; else they are measured first.  The lists
+        stay in ``lists`` (idx, count)."""
+        had = None if self.k_mean is None else self.k_mean.shape[1]
+        if not remeasure and had != -(-self.S // k_block):
+            raise ValueError("remeasure=False needs the block means of set_projection with this k_block")
+        self._means(k_block)
+        if remeasure:
+            p = norm_rope_params(self.Q, self.K, norm=False, q_block=DT_TILE, k_block=k_block)
+            dt_qk_norm_rope(p, self.Q, self.K, None, None, None, None, None, None, None, self.q_mean, self.k_mean, stream)
+        nq, nk = self.q_mean.shape[1], self.k_mean.shape[1]
+        if self.lists is None or self.lists[0].shape != (self.H, nq, topk):
+            self.lists = (torch.empty((self.H, nq, topk), dtype=torch.int32, device=self.device),
+                          torch.empty((self.H, nq), dtype=torch.int32, device=self.device))
+        idx, count = self.lists
+        dt_block_select(select_params(self.H, self.H, nq, nk, self.D, topk, keep_first, keep_last, margin), self.q_mean,
+                        self.k_mean, idx, count, stream)
+        dt_attn_block_sparse(sparse_params(self.Q, self.K, self.V, self.O, k_block, topk), self.Q, self.K, self.V, idx,
+                             count, self.O, self.L, self.status, stream)
 
     def _mark_plan_read(self, st) -> None:
         """Record that the launches issued so far on `st` read d_plan."""
