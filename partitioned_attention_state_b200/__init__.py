@@ -373,53 +373,74 @@ def dt_window_residual(op, H, S, D, O_full, O_win, R, O, d_status=None, stream=N
 # would be read or written out of bounds on the device) and run on the tensors'
 # device: on `stream` where given, else on that device's current stream.
 
+_TYPES: dict = {}           # torch element type -> DT_TYPE_*, and back; filled with _torch by _init
+_torch = None
+
+
+def _init():
+    """torch, imported on the first call that takes tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        for code, ty in ((DT_TYPE_BF16, torch.bfloat16), (DT_TYPE_F16, torch.float16), (DT_TYPE_F32, torch.float32)):
+            _TYPES[ty], _TYPES[code] = code, ty
+        _torch = torch
+    return _torch
+
+
 def _type_of(t) -> int:
-    import torch
     try:
-        return {torch.bfloat16: DT_TYPE_BF16, torch.float16: DT_TYPE_F16, torch.float32: DT_TYPE_F32}[t.dtype]
+        return _TYPES[t.dtype]
     except KeyError:
         raise TypeError(f"unsupported element type {t.dtype}") from None
 
 
-def _heads(t, name: str) -> "Strides":
-    """Strides of a [heads][rows][D] tensor or view whose rows are contiguous."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+def _heads(t, name: str):
+    """(head, row) strides of a [heads][rows][D] tensor or view whose rows are contiguous."""
+    st = t.stride()
+    if len(st) != 3 or (st[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{name}: expected [heads][rows][D] with contiguous rows, got {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
-    return Strides(t.stride(0), t.stride(1))
+                         f"with strides {st}")
+    return st[:2]
 
 
-def _match(t, shape, dtype, name: str, like=None) -> None:
-    """Raise unless t is a contiguous tensor of this shape and type (on like's device)."""
-    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)} "
-                         f"with strides {t.stride()}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
+# The checks below run in every call, so they compare whole tuples and look closer only when those differ.
+def _match(t, shape, dtype, name: str, device: int) -> None:
+    """Raise unless t is a contiguous tensor of this shape and type on this device."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{name}: expected contiguous {dtype} {shape} on device {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()} on device {t.get_device()}")
 
 
-def _match_heads(t, shape, strides, ty: int, name: str, like=None) -> None:
+def _match_heads(t, shape, strides, dtype, name: str, device: int) -> None:
     """Raise unless t is the [heads][rows][D] tensor that the parameters were made for."""
-    if tuple(t.shape) != shape or _type_of(t) != ty or (t.shape[2] > 1 and t.stride(2) != 1) or \
-            (shape[0] > 1 and t.stride(0) != strides.head) or (shape[1] > 1 and t.stride(1) != strides.row):
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} is not what the parameters "
-                         f"describe: {shape}, head stride {strides.head}, row stride {strides.row}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, not on {like.device}")
+    ok = t.shape == shape and t.dtype is dtype and t.get_device() == device
+    if ok:
+        st = t.stride()
+        ok = (st[0] == strides.head or shape[0] <= 1) and (st[1] == strides.row or shape[1] <= 1) and \
+             (st[2] == 1 or shape[2] <= 1)
+    if not ok:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} on device {t.get_device()} is "
+                         f"not what the parameters describe: {dtype} {shape}, head stride {strides.head}, row stride "
+                         f"{strides.row}, on device {device}")
 
 
-def _call(name: str, like, stream, p, *args) -> None:
-    """One C call with like's device current (launches go to the current device)."""
-    import torch
-    if not like.is_cuda:
-        raise ValueError(f"{name}: expected CUDA tensors, got one on {like.device}")
+def _call(name: str, device: int, stream, p, *args) -> None:
+    """One C call with the tensors' device current (launches go to the current device)."""
+    if device < 0:
+        raise ValueError(f"{name}: expected CUDA tensors")
     f = getattr(load(), name)
-    if like.device.index == torch.cuda.current_device():
-        status = f(ctypes.byref(p), *args, _stream(stream))
+    if stream is None:          # the raw handle of the device's current stream, without a Stream object
+        raw = _torch._C._cuda_getCurrentRawStream(device)
     else:
-        with torch.cuda.device(like.device):
-            status = f(ctypes.byref(p), *args, _stream(stream))
-    _check(status, name)
+        raw = getattr(stream, "cuda_stream", stream)
+    if device == _torch.cuda.current_device():
+        status = f(ctypes.byref(p), *args, raw)
+    else:
+        with _torch.cuda.device(device):
+            status = f(ctypes.byref(p), *args, raw)
+    if status != DT_OK:
+        raise DtError(status, name)
 
 
 def rope_params(S: int, axes, base: float = 10000.0) -> RopeParams:
@@ -432,10 +453,10 @@ def rope_params(S: int, axes, base: float = 10000.0) -> RopeParams:
 
 def dt_rope_table(p: RopeParams, pos, table, stream=None) -> None:
     """pos: int32 [axes][S]; table: float32 [S][rot/2][2], written with (cos, sin)."""
-    import torch
-    _match(pos, (p.n_axes, p.S), torch.int32, "pos")
-    _match(table, (p.S, sum(p.dim[:p.n_axes]) // 2, 2), torch.float32, "table", pos)
-    _call("dt_rope_table", pos, stream, p, _ptr(pos), _ptr(table))
+    torch, dev, n = _init(), pos.get_device(), p.n_axes
+    _match(pos, (n, p.S), torch.int32, "pos", dev)
+    _match(table, (p.S, sum(p.dim[:n]) // 2, 2), torch.float32, "table", dev)
+    _call("dt_rope_table", dev, stream, p, pos.data_ptr(), table.data_ptr())
 
 
 def norm_rope_params(q=None, k=None, v=None, Q=None, K=None, V=None, rot: int = 0,
@@ -444,44 +465,48 @@ def norm_rope_params(q=None, k=None, v=None, Q=None, K=None, V=None, rot: int = 
     """Parameters of dt_qk_norm_rope for tensors (or views) laid out like these:
     q [H][S][D], k and v [Hkv][S][D] inputs, Q, K, V outputs; a part may be
     None.  x.view(S, heads, D).transpose(0, 1) is a token-major projection."""
-    ins, outs = [t for t in (q, k, v) if t is not None], [t for t in (Q, K, V) if t is not None]
-    if not ins:
+    _init()
+    first = q if q is not None else k if k is not None else v
+    if first is None:
         raise ValueError("no input")
-    S, D = ins[0].shape[1], ins[0].shape[2]
-    ity = _type_of(ins[0])
-    p = NormRopeParams(S=S, D=D, H=0 if q is None else q.shape[0],
-                       Hkv=0 if k is None and v is None else (k if k is not None else v).shape[0], rot=rot,
-                       pairing=pairing, in_type=ity, out_type=_type_of(outs[0]) if outs else ity, norm=int(norm),
-                       q_block=q_block, k_block=k_block, eps=eps)
-    for n, t in (("q_in", q), ("k_in", k), ("v_in", v), ("q_out", Q), ("k_out", K), ("v_out", V)):
-        if t is not None:
-            setattr(p, n, _heads(t, n))
-    return p
+    out = Q if Q is not None else K if K is not None else V
+    kv = k if k is not None else v
+    _, S, D = first.shape
+    ity = _type_of(first)
+    return NormRopeParams(S, D, 0 if q is None else q.shape[0], 0 if kv is None else kv.shape[0], rot, pairing, ity,
+                          ity if out is None else _type_of(out), int(norm), q_block, k_block, eps,
+                          *[(0, 0) if t is None else _heads(t, n) for n, t in
+                            (("q", q), ("k", k), ("v", v), ("Q", Q), ("K", K), ("V", V))])
 
 
 def dt_qk_norm_rope(p: NormRopeParams, q, k, v, wq, wk, table, Q, K, V, q_mean=None, k_mean=None, stream=None) -> None:
     """Per-head RMS norm, rotation, layout change and block means in one pass
     (see norm_rope_params).  wq, wk: float32 [D] or None; table: dt_rope_table's,
     None with rot = 0; q_mean, k_mean: float32 [heads][blocks][D] or None."""
-    import torch
-    like = next((t for t in (q, k, v) if t is not None), None)
-    if like is None:
+    f32 = _init().float32
+    first = q if q is not None else k if k is not None else v
+    if first is None:
         raise ValueError("no input")
-    for t, n, heads, ty in ((q, "q_in", p.H, p.in_type), (k, "k_in", p.Hkv, p.in_type), (v, "v_in", p.Hkv, p.in_type),
-                            (Q, "q_out", p.H, p.out_type), (K, "k_out", p.Hkv, p.out_type),
-                            (V, "v_out", p.Hkv, p.out_type)):
+    dev, S, D, rot = first.get_device(), p.S, p.D, p.rot
+    qs, ks, ity, oty = (p.H, S, D), (p.Hkv, S, D), _TYPES.get(p.in_type), _TYPES.get(p.out_type)
+    ptr = []
+    for t, shape, n, ty in ((q, qs, "q_in", ity), (k, ks, "k_in", ity), (v, ks, "v_in", ity)):
         if t is not None:
-            _match_heads(t, (heads, p.S, p.D), getattr(p, n), ty, n, like)
-    for t, n in ((wq, "wq"), (wk, "wk")):
+            _match_heads(t, shape, getattr(p, n), ty, n, dev)
+        ptr.append(None if t is None else t.data_ptr())
+    for t, shape, n in ((wq, (D,), "wq"), (wk, (D,), "wk"), (table if rot else None, (S, rot // 2, 2), "table")):
         if t is not None:
-            _match(t, (p.D,), torch.float32, n, like)
-    if p.rot and table is not None:
-        _match(table, (p.S, p.rot // 2, 2), torch.float32, "table", like)
-    for t, n, heads, block in ((q_mean, "q_mean", p.H, p.q_block), (k_mean, "k_mean", p.Hkv, p.k_block)):
+            _match(t, shape, f32, n, dev)
+        ptr.append(None if t is None else t.data_ptr())
+    for t, shape, n in ((Q, qs, "q_out"), (K, ks, "k_out"), (V, ks, "v_out")):
+        if t is not None:
+            _match_heads(t, shape, getattr(p, n), oty, n, dev)
+        ptr.append(None if t is None else t.data_ptr())
+    for t, heads, block, n in ((q_mean, p.H, p.q_block, "q_mean"), (k_mean, p.Hkv, p.k_block, "k_mean")):
         if t is not None and block > 0:
-            _match(t, (heads, -(-p.S // block), p.D), torch.float32, n, like)
-    _call("dt_qk_norm_rope", like, stream, p, _ptr(q), _ptr(k), _ptr(v), _ptr(wq), _ptr(wk), _ptr(table), _ptr(Q),
-          _ptr(K), _ptr(V), _ptr(q_mean), _ptr(k_mean))
+            _match(t, (heads, -(-S // block), D), f32, n, dev)
+        ptr.append(None if t is None else t.data_ptr())
+    _call("dt_qk_norm_rope", dev, stream, p, *ptr)
 
 
 def select_params(H: int, Hkv: int, nq: int, nk: int, D: int, topk: int, keep_first: int = 0, keep_last: int = 0,
@@ -493,22 +518,22 @@ def dt_block_select(p: SelectParams, q_mean, k_mean, idx, count, stream=None) ->
     """Lists of key blocks by the scores of block means.  q_mean float32
     [H][nq][D], k_mean float32 [Hkv][nk][D]; idx int32 [H][nq][topk] and count
     int32 [H][nq] are written."""
-    import torch
-    _match(q_mean, (p.H, p.nq, p.D), torch.float32, "q_mean")
-    _match(k_mean, (p.Hkv, p.nk, p.D), torch.float32, "k_mean", q_mean)
-    _match(idx, (p.H, p.nq, p.topk), torch.int32, "idx", q_mean)
-    _match(count, (p.H, p.nq), torch.int32, "count", q_mean)
-    _call("dt_block_select", q_mean, stream, p, _ptr(q_mean), _ptr(k_mean), _ptr(idx), _ptr(count))
+    torch, dev, H, nq, D = _init(), q_mean.get_device(), p.H, p.nq, p.D
+    _match(q_mean, (H, nq, D), torch.float32, "q_mean", dev)
+    _match(k_mean, (p.Hkv, p.nk, D), torch.float32, "k_mean", dev)
+    _match(idx, (H, nq, p.topk), torch.int32, "idx", dev)
+    _match(count, (H, nq), torch.int32, "count", dev)
+    _call("dt_block_select", dev, stream, p, q_mean.data_ptr(), k_mean.data_ptr(), idx.data_ptr(), count.data_ptr())
 
 
 def sparse_params(Q, K, V, O, k_block: int = 64, cap: int = 0) -> SparseParams:
     """Parameters of dt_attn_block_sparse for tensors (or views) laid out like
     these: Q, O [H][Sq][D], K, V [Hkv][Sk][D]; cap entries per list."""
-    p = SparseParams(H=Q.shape[0], Hkv=K.shape[0], Sq=Q.shape[1], Sk=K.shape[1], D=Q.shape[2], k_block=k_block,
-                     cap=cap, type=_type_of(Q), out_type=_type_of(O))
-    for n, t in (("q", Q), ("k", K), ("v", V), ("o", O)):
-        setattr(p, n, _heads(t, n))
-    return p
+    _init()
+    H, Sq, D = Q.shape
+    Hkv, Sk, _ = K.shape
+    return SparseParams(H, Hkv, Sq, Sk, D, k_block, cap, _type_of(Q), _type_of(O), _heads(Q, "Q"), _heads(K, "K"),
+                        _heads(V, "V"), _heads(O, "O"))
 
 
 def dt_attn_block_sparse(p: SparseParams, Q, K, V, idx, count, O, L, d_status, stream=None) -> None:
@@ -516,19 +541,21 @@ def dt_attn_block_sparse(p: SparseParams, Q, K, V, idx, count, O, L, d_status, s
     the state (O, L).  idx int32 [H][ceil(Sq/128)][cap], count int32
     [H][ceil(Sq/128)] or None (cap entries each), L float32 [H][Sq], d_status
     int32 device status word."""
-    import torch
-    for t, n, shape, ty in ((Q, "q", (p.H, p.Sq, p.D), p.type), (K, "k", (p.Hkv, p.Sk, p.D), p.type),
-                            (V, "v", (p.Hkv, p.Sk, p.D), p.type), (O, "o", (p.H, p.Sq, p.D), p.out_type)):
-        _match_heads(t, shape, getattr(p, n), ty, n.upper(), Q)
-    nqb = -(-p.Sq // DT_TILE)
-    _match(idx, (p.H, nqb, p.cap), torch.int32, "idx", Q)
+    torch, dev, H, Sq, D = _init(), Q.get_device(), p.H, p.Sq, p.D
+    qs, ks, ty = (H, Sq, D), (p.Hkv, p.Sk, D), _TYPES.get(p.type)
+    _match_heads(Q, qs, p.q, ty, "Q", dev)
+    _match_heads(K, ks, p.k, ty, "K", dev)
+    _match_heads(V, ks, p.v, ty, "V", dev)
+    _match_heads(O, qs, p.o, _TYPES.get(p.out_type), "O", dev)
+    nqb = -(-Sq // DT_TILE)
+    _match(idx, (H, nqb, p.cap), torch.int32, "idx", dev)
     if count is not None:
-        _match(count, (p.H, nqb), torch.int32, "count", Q)
-    _match(L, (p.H, p.Sq), torch.float32, "L", Q)
-    if d_status.dtype != torch.int32 or d_status.numel() < 1 or d_status.device != Q.device:
+        _match(count, (H, nqb), torch.int32, "count", dev)
+    _match(L, (H, Sq), torch.float32, "L", dev)
+    if d_status.dtype is not torch.int32 or d_status.numel() < 1 or d_status.get_device() != dev:
         raise ValueError("d_status: expected an int32 tensor on the inputs' device")
-    _call("dt_attn_block_sparse", Q, stream, p, _ptr(Q), _ptr(K), _ptr(V), _ptr(idx), _ptr(count), _ptr(O), _ptr(L),
-          _ptr(d_status))
+    _call("dt_attn_block_sparse", dev, stream, p, Q.data_ptr(), K.data_ptr(), V.data_ptr(), idx.data_ptr(),
+          None if count is None else count.data_ptr(), O.data_ptr(), L.data_ptr(), d_status.data_ptr())
 
 
 def dt_set_wait_limit_ns(ns: int) -> None:

@@ -368,11 +368,15 @@ extern "C" int dt_rope_table(const dt_rope_params* p, const int32_t* pos, float*
   a.pos = pos;
   a.table = table;
   a.S = p->S;
-  for (int x = 0; x < p->n_axes; ++x)
-    for (int j = 0; j < p->dim[x] / 2; ++j) {
-      a.turns[a.pairs] = pow(p->base, -2.0 * j / p->dim[x]) / 6.283185307179586476925;
+  for (int x = 0; x < p->n_axes; ++x) {
+    // powers of one ratio: 128 extended-precision products stay below 2^-56
+    const long double ratio = powl((long double)p->base, -2.0L / p->dim[x]);
+    long double t = 1.0L / 6.283185307179586476925L;
+    for (int j = 0; j < p->dim[x] / 2; ++j, t *= ratio) {
+      a.turns[a.pairs] = (uint64_t)ldexpl(t - floorl(t), 64);       // whole turns do not matter
       a.axis[a.pairs++] = (uint8_t)x;
     }
+  }
   return dt::launch_rope_table(a, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -127,41 +127,47 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, int b_mn) {
 }
 
 // One item's list: entries [0, n), of which this CTA takes tiles [t0, t1).
-struct Item {
-  int h, q0, rows, n, t0, t1;
-  const int32_t* list;
-};
-__device__ __forceinline__ Item get_item(const SparseParams& p, int item, int rank) {
+// The list's length and its first entries are loaded an item ahead, and every
+// other entry a tile ahead: a load from L2 costs as much as a third of a tile,
+// and two one after another at every item cost each role 1-2 us.
+struct Item { int h, q0, rows, n, t0, t1; };
+__device__ __forceinline__ int load_count(const SparseParams& p, int item) {
+  return p.count && item < p.H * p.nqb ? __ldg(p.count + item) : p.cap;
+}
+__device__ __forceinline__ Item make_item(const SparseParams& p, int item, int rank, int count) {
   Item it;
   it.h = item / p.nqb;
-  const int qb = item - it.h * p.nqb;
-  it.q0 = qb * kTile;
+  it.q0 = (item - it.h * p.nqb) * kTile;
   it.rows = imin(kTile, p.Sq - it.q0);
-  int n = p.count ? __ldg(p.count + item) : p.cap;
-  it.n = imin(imax(n, 0), p.cap);
-  it.list = p.idx + (int64_t)item * p.cap;
+  it.n = imin(imax(count, 0), p.cap);
   const int nt = (it.n + p.per_tile - 1) / p.per_tile;
-  it.t0 = (int)((int64_t)nt * rank / p.split);
-  it.t1 = (int)((int64_t)nt * (rank + 1) / p.split);
+  it.t0 = p.split == 1 ? 0 : (int)((int64_t)nt * rank / p.split);
+  it.t1 = p.split == 1 ? nt : (int)((int64_t)nt * (rank + 1) / p.split);
   return it;
+}
+// The entries of tile t of an item's list, as loaded (none past the list's allocation).
+struct Entries { int a, b; };
+__device__ __forceinline__ Entries load_entries(const SparseParams& p, int item, int t) {
+  Entries e = {-1, -1};
+  const int i = t * p.per_tile;
+  if (item < p.H * p.nqb && i < p.cap) {
+    const int32_t* l = p.idx + (int64_t)item * p.cap + i;
+    e.a = __ldg(l);
+    if (p.per_tile == 2 && i + 1 < p.cap) e.b = __ldg(l + 1);
+  }
+  return e;
 }
 // First key rows of the two 64-row halves of tile t; Sk (nothing there) for an
 // entry outside the sequence, -1 for the half that an odd list does not have.
 struct Halves { int r0, r1; };
-__device__ __forceinline__ Halves tile_halves(const SparseParams& p, const Item& it, int t) {
+__device__ __forceinline__ Halves tile_halves(const SparseParams& p, const Item& it, int t, Entries e) {
   Halves v;
   if (p.per_tile == 1) {
-    const int b = __ldg(it.list + t);
-    v.r0 = (unsigned)b < (unsigned)p.nkb ? b * 128 : p.Sk;
+    v.r0 = (unsigned)e.a < (unsigned)p.nkb ? e.a * 128 : p.Sk;
     v.r1 = v.r0 < p.Sk - 64 ? v.r0 + 64 : p.Sk;
   } else {
-    const int b0 = __ldg(it.list + 2 * t);
-    v.r0 = (unsigned)b0 < (unsigned)p.nkb ? b0 * 64 : p.Sk;
-    v.r1 = -1;
-    if (2 * t + 1 < it.n) {
-      const int b1 = __ldg(it.list + 2 * t + 1);
-      v.r1 = (unsigned)b1 < (unsigned)p.nkb ? b1 * 64 : p.Sk;
-    }
+    v.r0 = (unsigned)e.a < (unsigned)p.nkb ? e.a * 64 : p.Sk;
+    v.r1 = 2 * t + 1 >= it.n ? -1 : ((unsigned)e.b < (unsigned)p.nkb ? e.b * 64 : p.Sk);
   }
   return v;
 }
@@ -287,9 +293,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
           if (C::kTail)
             tma_load_3d_hint(tile + C::kN64 * C::kBlk + half * (C::kTailBytes / 2), t16, bar, 64 * C::kN64, row0, h, pol);
         };
+        int count = load_count(p, item0);
+        Entries first = load_entries(p, item0, make_item(p, item0, rank, count).t0);
         for (int item = item0; item < items; item += istep) {
-          const Item it = get_item(p, item, rank);
-          if (is_k && rank == 0 && p.count && __ldg(p.count + item) != it.n) atomicCAS(p.status, 0, DT_ERR_INVALID);
+          const Item it = make_item(p, item, rank, count);
+          if (is_k && rank == 0 && count != it.n) atomicCAS(p.status, 0, DT_ERR_INVALID);
+          Entries nxt = first;
+          count = load_count(p, item + istep);
+          first = load_entries(p, item + istep, 0);
           if (it.t0 == it.t1) continue;
           if (is_k) {
             const uint32_t b = nq % C::kNQ;
@@ -303,10 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
             ++nq;
           }
           const int hk = it.h / p.per_kv;
-          Halves nxt = tile_halves(p, it, it.t0);
           for (int t = it.t0; t < it.t1; ++t, ++g) {
-            const Halves v = nxt;
-            if (t + 1 < it.t1) nxt = tile_halves(p, it, t + 1);
+            const Halves v = tile_halves(p, it, t, nxt);
+            if (t + 1 < it.t1) nxt = load_entries(p, item, t + 1);
             if (is_k && (v.r0 >= p.Sk || (p.per_tile == 2 && v.r1 >= p.Sk))) atomicCAS(p.status, 0, DT_ERR_INVALID);
             const uint32_t st = g % ns;
             if (g >= ns && !mbar_wait(&empty[st], ((g / ns) - 1) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim))
@@ -340,8 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         const uint32_t aK = smem_u32(sK);
         uint32_t g = 0, nq = 0;
         bool ok = true;
+        int count = load_count(p, item0);
         for (int item = item0; item < items && ok; item += istep) {
-          const Item it = get_item(p, item, rank);
+          const Item it = make_item(p, item, rank, count);
+          count = load_count(p, item + istep);
           if (it.t0 == it.t1) continue;
           const uint32_t qb = nq % C::kNQ;
           const uint32_t aQ = smem_u32(sQ) + qb * C::kTileBytes;
@@ -398,8 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         const uint32_t aV = smem_u32(sV);
         uint32_t g = 0, nq = 0;
         bool ok = true;
+        int count = load_count(p, item0);
         for (int item = item0; item < items && ok; item += istep) {
-          const Item it = get_item(p, item, rank);
+          const Item it = make_item(p, item, rank, count);
+          count = load_count(p, item + istep);
           if (it.t0 == it.t1) continue;
           for (int t = it.t0; t < it.t1 && ok; ++t, ++g) {
             const uint32_t sb = g % C::kNS, st = g % C::kNV;
@@ -449,15 +463,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     const uint32_t lane_base = static_cast<uint32_t>(rbase) << 16;
     const float sl2 = p.scale_log2;
     uint32_t g = 0, nq = 0;
+    int count = load_count(p, item0);
+    Entries first = load_entries(p, item0, make_item(p, item0, rank, count).t0);
     for (int item = item0; item < items; item += istep) {
-      const Item it = get_item(p, item, rank);
+      const Item it = make_item(p, item, rank, count);
+      Entries nxt = first;
+      count = load_count(p, item + istep);
+      first = load_entries(p, item + istep, 0);
       if (it.t0 == it.t1) continue;
       const bool idle = rbase >= it.rows;          // none of this warp's rows exist: hand the tiles on
       float ma = neg_inf(), mb = neg_inf();         // running max (log2 units)
       uint64_t la[2] = {0ull, 0ull}, lb[2] = {0ull, 0ull};      // packed pairs of partial row sums
       for (int t = it.t0; t < it.t1; ++t, ++g) {
         const uint32_t sb = g % C::kNS;
-        const Halves hv = tile_halves(p, it, t);   // its latency passes under the wait
+        const Halves hv = tile_halves(p, it, t, nxt);
+        if (t + 1 < it.t1) nxt = load_entries(p, item, t + 1);
         if (!warp_wait(&bars[C::bSFull + sb], (g / C::kNS) & 1, abort_flag, p.status, lim)) goto sm_done;
         if (idle) {
           mbar_arrive(&bars[C::bPFull + sb]);
@@ -578,8 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     const int r = (warp - kWarpEpi) * 32 + lane;          // tile row of this thread
     const uint32_t oaddr = tmem + (static_cast<uint32_t>((warp - kWarpEpi) * 32) << 16) + C::kColO;
     uint32_t nq = 0;
+    int count = load_count(p, item0);
     for (int item = item0; item < items; item += istep) {
-      const Item it = get_item(p, item, rank);
+      const Item it = make_item(p, item, rank, count);
+      count = load_count(p, item + istep);
       const bool valid = r < it.rows;
       const int64_t orow = it.h * p.o_head + (int64_t)(it.q0 + r) * p.o_row;
       float* lrow = p.L + (int64_t)it.h * p.Sq + it.q0 + r;
@@ -638,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     __syncwarp();
     cluster_sync_all();
     if (warp >= kWarpEpi && warp < kWarpMma && !*abort_flag) {
-      const Item it = get_item(p, item0, rank);
+      const Item it = make_item(p, item0, rank, load_count(p, item0));
       const uint32_t a_m = smem_u32(stat_m), a_l = smem_u32(stat_l), a_o = smem_u32(sK);
       const int nchunk = it.rows * (D / 8);
       for (int i = (threadIdx.x - kWarpEpi * 32) * p.split + rank; i < nchunk; i += 128 * p.split) {

@@ -11,38 +11,51 @@
 #include <stdint.h>
 
 #include "../../include/dt.h"
+#include "sm100.cuh"
 #include "token_ops.h"
 
 namespace dt {
 namespace {
 
+using namespace sm100;
+
 int launched() { return cudaGetLastError() == cudaSuccess ? DT_OK : DT_ERR_CUDA; }
 int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------------ rotation table
-// cos and sin of 2 pi t, t = pos * turns.  The product and its reduction to
-// the nearest whole turn are in 64 bits (t - rint(t) is exact), so the angle of
-// a position of 2^31 still has 2^-22 turns of error or less.  The fraction is
-// split into two floats: sincospif of the high part, then the angle-sum
-// formula to first order for the low one (|low| <= 2^-25 turns, so the
-// second-order term is below 2^-46): full fp32 accuracy without the 64-bit
-// sincos, which alone would cost four times the table's HBM time.
-// One thread per two pairs of a token (16 bytes of the table).
-__global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
+// cos and sin of 2 pi t, t = pos * turns, where only t's fraction counts: with
+// turns as a 64-bit binary fraction T, pos * T mod 2^64 is that fraction
+// without any reduction, off by at most |pos| 2^-65 turns, and needs no 64-bit
+// floating point.  Its upper 32 bits, signed, are split into a float and the
+// remainder: sincospif of the float, then the angle-sum formula to first order
+// for the remainder (at most 2^-25 turns, so the second-order term is below
+// 2^-45): full fp32 accuracy.  A CTA owns kRopeTokens tokens, a thread two pairs of
+// a token (16 bytes of the table) at a time; T and the axes lie in shared
+// memory, since lanes with different pairs would serialise on the parameter bank.
+constexpr int kRopeThreads = 256, kRopeTokens = 32;
+
+__global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
+  __shared__ uint64_t turns[kMaxPairs];
+  __shared__ int axis[kMaxPairs];
+  for (int i = threadIdx.x; i < a.pairs; i += kRopeThreads) {
+    turns[i] = a.turns[i];
+    axis[i] = a.axis[i];
+  }
+  __syncthreads();
   const int halfp = (a.pairs + 1) / 2;
-  const int64_t n = (int64_t)a.S * halfp;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
-    const int s = (int)(i / halfp), p0 = 2 * (int)(i - (int64_t)s * halfp);
+  const int s0 = blockIdx.x * kRopeTokens, n = min(kRopeTokens, a.S - s0) * halfp;
+  for (int i = threadIdx.x; i < n; i += kRopeThreads) {
+    const int ds = i / halfp, p0 = 2 * (i - ds * halfp), s = s0 + ds;
     float out[4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int pr = p0 + e < a.pairs ? p0 + e : p0;
-      const double t = (double)__ldg(a.pos + (int64_t)a.axis[pr] * a.S + s) * a.turns[pr];
-      const double f = t - rint(t);
-      const float hi = (float)f, lo = (float)(f - (double)hi);
+      const int pr = min(p0 + e, a.pairs - 1);
+      const int64_t pos = __ldg(a.pos + (int64_t)axis[pr] * a.S + s);
+      const int u = (int)(((uint64_t)pos * turns[pr]) >> 32);           // 2^-32 turns, [-1/2, 1/2)
+      const float hi = (float)u, lo = (float)(u - (int)hi);
       float sn, cs;
-      sincospif(2.f * hi, &sn, &cs);
-      const float d = 6.2831853071795865f * lo;
+      sincospif(hi * 0x1p-31f, &sn, &cs);
+      const float d = lo * 1.46291807926715968e-9f;                     // 2 pi 2^-32
       out[2 * e] = fmaf(-d, sn, cs);
       out[2 * e + 1] = fmaf(d, cs, sn);
     }
@@ -94,163 +107,188 @@ __device__ __forceinline__ uint2 narrow4<__half>(const float* x) {
 }
 // 8 elements as two groups of 4; one 16-byte access where they are adjacent 16-bit elements
 template <typename T, bool SPLIT>
-__device__ __forceinline__ void load8(const T* row, int c0, int c1, typename Vec4<T>::type (&v)[2]) {
+__device__ __forceinline__ void load8(const T* at, int gap, typename Vec4<T>::type (&v)[2]) {
   using V = typename Vec4<T>::type;
   if (sizeof(T) == 2 && !SPLIT) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(row + c0));
-    *reinterpret_cast<uint4*>(v) = u;
+    *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(at));
   } else {
-    v[0] = __ldcs(reinterpret_cast<const V*>(row + c0));
-    v[1] = __ldcs(reinterpret_cast<const V*>(row + c1));
+    v[0] = __ldcs(reinterpret_cast<const V*>(at));
+    v[1] = __ldcs(reinterpret_cast<const V*>(at + gap));
   }
 }
 template <typename T, bool SPLIT>
-__device__ __forceinline__ void store8(T* row, int c0, int c1, const float* x) {
+__device__ __forceinline__ void store8(T* at, int gap, const float* x) {
   using V = typename Vec4<T>::type;
   V v[2] = {narrow4<T>(x), narrow4<T>(x + 4)};
   if (sizeof(T) == 2 && !SPLIT) {
-    *reinterpret_cast<uint4*>(row + c0) = *reinterpret_cast<const uint4*>(v);
+    *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(v);
   } else {
-    *reinterpret_cast<V*>(row + c0) = v[0];
-    *reinterpret_cast<V*>(row + c1) = v[1];
+    *reinterpret_cast<V*>(at) = v[0];
+    *reinterpret_cast<V*>(at + gap) = v[1];
   }
 }
 
-// A CTA owns 128 consecutive tokens and walks a run of heads (of all parts:
-// queries, then keys, then values), so the tokens' 64 KB of rotation (D = 128)
-// come from L2 once per CTA and from L1 for its other heads: read per head from
-// L2 they would be twice the bytes of the 16-bit rows.  LPR lanes hold a row, 8
-// elements each.  An element's partner in its pair is always in the same
-// thread (HALVES: 4 elements from each half), so the row's sum of squares is
-// the only exchange, by shuffles.  A head's rows are loaded before they are
-// stored and by the thread that stores them (in-place calls).  Block means:
-// sums over a thread's rows, then over the lanes of the same columns, then
-// over the warps through shared memory, in a fixed order.
-constexpr int kNormThreads = 512;
+// A warp owns a head and a run of consecutive tokens: all 128 of a tile, or, when
+// that would leave SMs idle, 1/wt of them (wt = 2, 4, 8 warps per head).  The
+// warps of a CTA take neighbouring heads, so that together they read whole
+// stretches of a token-major row (8 heads of 128: 2 KB) and write whole
+// stretches of a head; a CTA per head, reading one 256-byte piece of every
+// row, reached 0.63 of the HBM rate on 40 heads of 128.  The tokens'
+// rotation comes from L2 once per CTA and from L1 for its other heads.  LPR
+// lanes hold a row, 8 elements each.  An element's partner in its pair is
+// always in the same thread (HALVES: 4 elements from each half), so the row's
+// sum of squares is the only exchange, by shuffles.  A row is loaded whole before
+// it is stored, by the warp that stores it (in-place calls).  Block means: sums over a
+// lane's rows, then over the lanes of the same columns, then over the warps of
+// the head through shared memory, in a fixed order.
+constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
 
 template <typename TI, typename TO, int LPR, bool HALVES>
-__global__ void __launch_bounds__(kNormThreads, 2) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int kRowsPerPass = kNormThreads / LPR;
-  constexpr int R = 64 / kRowsPerPass;              // rows of a 64-row half a thread owns: 1 for LPR 8, 2 for 16
-  constexpr int kWarps = kNormThreads / 32;
-  __shared__ float part[2][kWarps][LPR * 8];        // block sums per warp, halves of the tile apart
+__global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+  constexpr int kTok = 32 / LPR;                    // tokens of a step
+  constexpr int kBatch = sizeof(TI) == 4 ? 2 : 4;   // steps whose rows are loaded together
+  // sums of each warp's segments (64 tokens, or the warp's run if shorter)
+  __shared__ float part[2 * kNormWarps][LPR * 8];
   const dt_norm_rope_params& p = a.p;
-  const int s0 = blockIdx.x * 128;
-  const int lane = threadIdx.x % LPR, rbase = threadIdx.x / LPR, warp = threadIdx.x / 32;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % LPR, sub = (threadIdx.x % 32) / LPR;
+  const int wh = kNormWarps / a.wt;                 // heads of the CTA
+  const int tile = blockIdx.x / a.groups, group = blockIdx.x - tile * a.groups;
+  const int hw = warp / a.wt, ws = warp - hw * a.wt;
+  const int run = 128 / a.wt, seg = min(run, 64);
+  const int hh = group * wh + hw;
+  const int s0 = tile * 128 + ws * run + sub;       // this lane's first token
   const bool on = 8 * lane < p.D;
   const bool turned = 8 * lane < p.rot;
   const int c0 = HALVES && turned ? 4 * lane : 8 * lane;
-  const int c1 = HALVES && turned ? p.rot / 2 + 4 * lane : 8 * lane + 4;
-  const int heads = p.H + 2 * p.Hkv;
-  const int h_end = min(heads, (int)(blockIdx.y + 1) * a.heads_per_cta);
+  const int gap = HALVES && turned ? p.rot / 2 : 4; // from the first 4 elements to the others
 
-  for (int hh = blockIdx.y * a.heads_per_cta; hh < h_end; ++hh) {
-    const int kind = hh < p.H ? 0 : (hh < p.H + p.Hkv ? 1 : 2);
-    const int h = kind == 0 ? hh : (kind == 1 ? hh - p.H : hh - p.H - p.Hkv);
-    const TI* in = static_cast<const TI*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v));
-    TO* out = static_cast<TO*>(kind == 0 ? a.Q : (kind == 1 ? a.K : a.V));
-    float* mean = kind == 0 ? a.q_mean : (kind == 1 ? a.k_mean : nullptr);
-    if (!in) continue;
+  const int kind = hh < p.H ? 0 : (hh < p.H + p.Hkv ? 1 : 2);
+  const int h = kind == 0 ? hh : (kind == 1 ? hh - p.H : hh - p.H - p.Hkv);
+  const TI* in = static_cast<const TI*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v));
+  TO* out = static_cast<TO*>(kind == 0 ? a.Q : (kind == 1 ? a.K : a.V));
+  float* mean = kind == 0 ? a.q_mean : (kind == 1 ? a.k_mean : nullptr);
+  if (hh < p.H + 2 * p.Hkv && in) {
     const dt_strides si = kind == 0 ? p.q_in : (kind == 1 ? p.k_in : p.v_in);
     const dt_strides so = kind == 0 ? p.q_out : (kind == 1 ? p.k_out : p.v_out);
+    const bool store = out != nullptr;
+    in += h * si.head + s0 * si.row + c0;
+    if (store) out += h * so.head + s0 * so.row + c0;
+    const int64_t istep = kTok * si.row, ostep = kTok * so.row;
+    int left = on ? p.S - s0 : 0;                   // rows from this lane's next to the end
+    const bool norm = kind < 2 && p.norm, turn = kind < 2 && turned;
+    const float* tr = a.table + ((int64_t)s0 * (p.rot / 2) + 4 * lane) * 2;
+    const int tstep = kTok * p.rot;
     const float* w = kind == 0 ? a.wq : a.wk;
-    in += h * si.head;
-    out += h * so.head;
-
     float wv[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    if (kind < 2 && p.norm && w && on) {
+    if (norm && w && on) {
       widen(__ldg(reinterpret_cast<const float4*>(w + c0)), wv);
-      widen(__ldg(reinterpret_cast<const float4*>(w + c1)), wv + 4);
+      widen(__ldg(reinterpret_cast<const float4*>(w + c0 + gap)), wv + 4);
     }
+    const uint64_t w2[4] = {pk2(wv[0], wv[1]), pk2(wv[2], wv[3]), pk2(wv[4], wv[5]), pk2(wv[6], wv[7])};
+#pragma unroll 1
+    for (int t0 = 0; t0 < run; t0 += seg) {
+      uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll 1
+      for (int t = 0; t < seg; t += kTok * kBatch) {
+        if (__all_sync(0xffffffffu, left <= 0)) break;
+        typename Vec4<TI>::type raw[kBatch][2];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      typename Vec4<TI>::type raw[R][2];
-      float4 cs[R][2];                              // (cos, sin) of the thread's 4 pairs
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int s = s0 + 64 * b + rbase + j * kRowsPerPass;
-        if (on && s < p.S) load8<TI, HALVES>(in + s * si.row, c0, c1, raw[j]);
-        else { raw[j][0] = {}; raw[j][1] = {}; }
-        if (kind < 2 && turned && s < p.S) {
-          const float4* t = reinterpret_cast<const float4*>(a.table + ((int64_t)s * (p.rot / 2) + 4 * lane) * 2);
-          cs[j][0] = __ldg(t);
-          cs[j][1] = __ldg(t + 1);
-        } else {
-          cs[j][0] = cs[j][1] = make_float4(1.f, 0.f, 1.f, 0.f);
+        for (int b = 0; b < kBatch; ++b) {
+          raw[b][0] = {};
+          raw[b][1] = {};
+          if (b * kTok < left) load8<TI, HALVES>(in, gap, raw[b]);
+          in += istep;
         }
-      }
-      float sum[8] = {};
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int s = s0 + 64 * b + rbase + j * kRowsPerPass;
-        float x[8];
-        widen4<TI>(raw[j][0], x);
-        widen4<TI>(raw[j][1], x + 4);
-        if (kind < 2) {
-          if (p.norm) {
-            float ss = 0.f;
+        for (int b = 0; b < kBatch; ++b) {
+          const bool live = b * kTok < left;
+          float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+          if (turn && live) {
+            u = __ldg(reinterpret_cast<const float4*>(tr));
+            v = __ldg(reinterpret_cast<const float4*>(tr) + 1);
+          }
+          tr += tstep;
+          float x[8];
+          widen4<TI>(raw[b][0], x);
+          widen4<TI>(raw[b][1], x + 4);
+          if (norm) {
+            uint64_t x2[4] = {pk2(x[0], x[1]), pk2(x[2], x[3]), pk2(x[4], x[5]), pk2(x[6], x[7])};
+            uint64_t ss2 = mul2(x2[0], x2[0]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            for (int e = 1; e < 4; ++e) ss2 = fma2(x2[e], x2[e], ss2);
+            float sa, sb;
+            upk2(ss2, sa, sb);
+            float ss = sa + sb;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = rsqrtf(ss / (float)p.D + p.eps);
+            const float r = rsqrtf(fmaf(ss, a.inv_d, p.eps));
+            const uint64_t r2 = pk2(r, r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * r * wv[e];
+            for (int e = 0; e < 4; ++e) upk2(mul2(mul2(x2[e], r2), w2[e]), x[2 * e], x[2 * e + 1]);
           }
-          if (turned) {
-            const float t[8] = {cs[j][0].x, cs[j][0].y, cs[j][0].z, cs[j][0].w,
-                                cs[j][1].x, cs[j][1].y, cs[j][1].z, cs[j][1].w};
+          if (turn) {
+            const float c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int ia = HALVES ? e : 2 * e, ib = HALVES ? e + 4 : 2 * e + 1;
               const float xa = x[ia], xb = x[ib];
-              x[ia] = fmaf(xa, t[2 * e], -(xb * t[2 * e + 1]));
-              x[ib] = fmaf(xa, t[2 * e + 1], xb * t[2 * e]);
+              x[ia] = fmaf(xa, c[2 * e], -(xb * c[2 * e + 1]));
+              x[ib] = fmaf(xa, c[2 * e + 1], xb * c[2 * e]);
             }
           }
-        }
-        if (on && s < p.S) {
-          if (a.store[kind]) store8<TO, HALVES>(out + s * so.row, c0, c1, x);
+          if (live) {
+            if (store) store8<TO, HALVES>(out, gap, x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] += x[e];
+            for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], pk2(x[2 * e], x[2 * e + 1]));
+          }
+          if (store) out += ostep;
         }
+        left -= kTok * kBatch;
       }
       if (mean) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) upk2(sum[e], v[2 * e], v[2 * e + 1]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
 #pragma unroll
-          for (int o = LPR; o < 32; o <<= 1) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+          for (int o = LPR; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
         }
-        if ((threadIdx.x & 31) < LPR) {
-          *reinterpret_cast<float4*>(&part[b][warp][8 * lane]) = make_float4(sum[0], sum[1], sum[2], sum[3]);
-          *reinterpret_cast<float4*>(&part[b][warp][8 * lane + 4]) = make_float4(sum[4], sum[5], sum[6], sum[7]);
+        if (sub == 0) {
+          float* dst = &part[2 * warp + (t0 > 0)][8 * lane];
+          *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
         }
       }
     }
-    if (mean) {
-      __syncthreads();
-      const int blk = kind == 0 ? p.q_block : p.k_block;
-      const int nblk = (p.S + blk - 1) / blk;
-      for (int i = threadIdx.x; i < 2 * LPR * 8; i += kNormThreads) {
-        const int b = i / (LPR * 8), c = i - b * (LPR * 8);      // c: lane-major position
-        const int r0 = s0 + 64 * b, n = min(blk, p.S - r0);
-        const int l8 = c / 8, e = c & 7;
-        if ((blk == 128 && b == 1) || n <= 0 || 8 * l8 >= p.D) continue;
-        float v = 0.f;
-        for (int k = 0; k < kWarps; ++k) v += part[b][k][c];
-        if (blk == 128)
-          for (int k = 0; k < kWarps; ++k) v += part[1][k][c];
-        const bool tl = HALVES && 8 * l8 < p.rot;
-        const int col = tl ? (e < 4 ? 4 * l8 + e : p.rot / 2 + 4 * l8 + e - 4) : 8 * l8 + e;
-        mean[((int64_t)h * nblk + r0 / blk) * p.D + col] = v / (float)n;
-      }
-      __syncthreads();
+  }
+  if (!a.q_mean && !a.k_mean) return;
+  __syncthreads();
+  // one thread per (head of the CTA, 64-token half, column); a 128-row block is written by its first half
+  for (int i = threadIdx.x; i < wh * 2 * LPR * 8; i += kNormThreads) {
+    const int hi = i / (2 * LPR * 8), b = (i / (LPR * 8)) & 1, c = i % (LPR * 8);   // c: lane-major position
+    const int hq = group * wh + hi;
+    float* m = hq < p.H ? a.q_mean : (hq < p.H + p.Hkv ? a.k_mean : nullptr);
+    if (!m || !(hq < p.H ? a.q : a.k)) continue;
+    const int blk = hq < p.H ? p.q_block : p.k_block, nblk = (p.S + blk - 1) / blk;
+    const int r0 = tile * 128 + 64 * b, n = min(blk, p.S - r0);
+    const int l8 = c / 8, e = c & 7;
+    if ((blk == 128 && b == 1) || n <= 0 || 8 * l8 >= p.D) continue;
+    // the slots of half b: with one warp per head its segments b, else the warps of that half, segment 0 of each
+    float v = 0.f;
+    for (int hb = b; hb < (blk == 128 ? 2 : b + 1); ++hb) {
+      if (a.wt == 1) v += part[2 * hi + hb][c];
+      else
+        for (int k = 0; k < a.wt / 2; ++k) v += part[2 * (hi * a.wt + hb * (a.wt / 2) + k)][c];
     }
+    const bool tl = HALVES && 8 * l8 < p.rot;
+    const int col = tl ? (e < 4 ? 4 * l8 + e : p.rot / 2 + 4 * l8 + e - 4) : 8 * l8 + e;
+    m[((int64_t)(hq < p.H ? hq : hq - p.H) * nblk + r0 / blk) * p.D + col] = v / (float)n;
   }
 }
 
 template <typename TI, typename TO>
-void norm_rope_dispatch(const NormRopeArgs& a, dim3 grid, cudaStream_t st) {
+void norm_rope_dispatch(const NormRopeArgs& a, unsigned grid, cudaStream_t st) {
   const bool hv = a.p.pairing == DT_ROPE_HALVES;
 #define DT_NR(LPR)                                                                                   \
   (hv ? qk_norm_rope_kernel<TI, TO, LPR, true><<<grid, kNormThreads, 0, st>>>(a)                      \
@@ -261,15 +299,21 @@ void norm_rope_dispatch(const NormRopeArgs& a, dim3 grid, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------ block selection
-// One CTA: kRows query blocks of one head against all its key blocks.
-// Scores: 64-bit FMAs (B200 issues half as many as fp32 ones) over tiles of 64
-// key blocks staged in shared memory as doubles, one key block and a quarter of
-// the rows per thread; then a warp per row finds the topk-th largest by a
-// radix selection over order-preserving 64-bit keys, and writes the chosen
-// blocks in increasing order by ballots.
-constexpr int kSelThreads = 256;
-constexpr int kSelTile = 64;                        // key blocks per staged tile
-constexpr int kSelPad = 1;                          // doubles between staged rows (bank spread)
+// One CTA: R query blocks of one head against all its key blocks.
+//
+// Scores on the 64-bit tensor cores (m8n8k4): fp32 operands widen exactly, a
+// product of two is exact, and only the sum rounds, at 2^-53.  A warp owns 16
+// key blocks at a time and R (8 or 16, padded with zero rows) query blocks; the
+// queries lie in shared memory as doubles, the keys come from L2 straight into
+// the fragments.  The order of a dot product's terms is free, so lane j of a
+// quad takes the consecutive columns 4j .. 4j+3 of each 16 for its 4 k-steps:
+// 16-byte loads on both sides instead of one element per step.
+//
+// Then a warp per row finds the topk-th largest by a radix selection, 8 bits a
+// pass from the highest bit in which the row's keys differ (order-preserving
+// 64-bit keys), ending as soon as a digit's keys are all wanted, and writes the
+// chosen blocks in increasing order by ballots.
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 
 // order-preserving key of a score; NaN counts as -infinity
 __device__ __forceinline__ uint64_t order_key(double x) {
@@ -278,120 +322,156 @@ __device__ __forceinline__ uint64_t order_key(double x) {
   const int64_t b = __double_as_longlong(x);
   return (uint64_t)(b < 0 ? ~b : (b | (int64_t)0x8000000000000000ull));
 }
+__device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
+               : "+d"(c[0]), "+d"(c[1]) : "d"(a), "d"(b));
+}
 
-template <int ROWS>
-__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const dt_select_params p, const float* q_mean,
-                                                                   const float* k_mean, int32_t* idx,
-                                                                   int32_t* count, int qtiles) {
+__host__ __device__ inline int select_ldq(int D) { return (D + 15) / 16 * 16 + 2; }   // doubles; +2 spreads the banks
+
+template <int MT>                                   // 8-row tiles of query blocks: R <= 8 * MT
+__global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_select_params p, const float* q_mean,
+                                                                      const float* k_mean, int32_t* idx,
+                                                                      int32_t* count, int qtiles, int R) {
   extern __shared__ double sm[];
-  const int D = p.D, ld = D + kSelPad;
-  double* sQ = sm;                                  // [ROWS][D]
-  double* sK = sQ + ROWS * D;                       // [kSelTile][ld]
-  uint64_t* keys = reinterpret_cast<uint64_t*>(sK + kSelTile * ld);      // [ROWS][nk]
-  __shared__ uint32_t hist[kSelThreads / 32][256];
-  const int h = blockIdx.x / qtiles, q0 = (blockIdx.x - h * qtiles) * ROWS;
-  const int rows = min(ROWS, p.nq - q0);
-  const float* km = k_mean + (int64_t)(h / (p.H / p.Hkv)) * p.nk * D;
+  __shared__ uint32_t hist[kSelWarps][256];
+  const int D = p.D, nk = p.nk, ldq = select_ldq(D);
+  double* sQ = sm;                                  // [8 * MT][ldq], zeros past the rows and columns
+  uint64_t* keys = reinterpret_cast<uint64_t*>(sQ + 8 * MT * ldq);       // [R][nk]
+  const int h = blockIdx.x / qtiles, q0 = (blockIdx.x - h * qtiles) * R;
+  const int rows = min(R, p.nq - q0);
+  const float* km = k_mean + (int64_t)(h / (p.H / p.Hkv)) * nk * D;
   const float* qm = q_mean + ((int64_t)h * p.nq + q0) * D;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, j = lane & 3;            // a fragment's row (query or key) and quad lane
   const double scale = 1.0 / sqrt((double)D);
 
-  for (int i = tid; i < ROWS * D; i += kSelThreads) sQ[i] = i < rows * D ? (double)qm[i] : 0.0;
-  for (int k0 = 0; k0 < p.nk; k0 += kSelTile) {
-    const int nt = min(kSelTile, p.nk - k0);
-    __syncthreads();
-    for (int i = tid; i < kSelTile * (D / 4); i += kSelThreads) {
-      const int r = i / (D / 4), c = 4 * (i - r * (D / 4));
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < nt) v = __ldg(reinterpret_cast<const float4*>(km + (int64_t)(k0 + r) * D + c));
-      double* d = sK + r * ld + c;
-      d[0] = v.x; d[1] = v.y; d[2] = v.z; d[3] = v.w;
-    }
-    __syncthreads();
-    // thread: key column tid % 64, rows tid/64, tid/64 + 4, ...
-    constexpr int RT = ROWS >= 4 ? ROWS / 4 : 1;
-    const int col = tid & 63, rg = tid >> 6;
-    if (rg < ROWS) {
-      double acc[RT] = {};
-      const double* kr = sK + col * ld;
-#pragma unroll 4
-      for (int d = 0; d < D; ++d) {
-        const double kv = kr[d];
+  for (int i = tid; i < 8 * MT * ldq; i += kSelThreads) {
+    const int r = i / ldq, c = i - r * ldq;
+    sQ[i] = r < rows && c < D ? (double)qm[(int64_t)r * D + c] : 0.0;
+  }
+  __syncthreads();
+  for (int n0 = 16 * warp; n0 < nk; n0 += 16 * kSelWarps) {
+    double acc[MT][2][2] = {};
+    const float* kr[2];
 #pragma unroll
-        for (int j = 0; j < RT; ++j) acc[j] = fma(sQ[(rg + 4 * j) * D + d], kv, acc[j]);
+    for (int n = 0; n < 2; ++n) kr[n] = km + (int64_t)min(n0 + 8 * n + g, nk - 1) * D;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k0 = 4 * j; k0 - 4 * j < D; k0 += 16) {
+      float4 kb[2];
+#pragma unroll
+      for (int n = 0; n < 2; ++n) kb[n] = k0 < D ? __ldg(reinterpret_cast<const float4*>(kr[n] + k0)) : zero;
+      double qa[MT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const double2* src = reinterpret_cast<const double2*>(sQ + (8 * m + g) * ldq + k0);
+        const double2 u = src[0], v = src[1];
+        qa[m][0] = u.x; qa[m][1] = u.y; qa[m][2] = v.x; qa[m][3] = v.y;
       }
-      if (col < nt)
 #pragma unroll
-        for (int j = 0; j < RT; ++j) keys[(int64_t)(rg + 4 * j) * p.nk + k0 + col] = order_key(acc[j] * scale);
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const double b = t == 0 ? kb[n].x : (t == 1 ? kb[n].y : (t == 2 ? kb[n].z : kb[n].w));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) mma_f64(acc[m][n], qa[m][t], b);
+        }
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = 8 * m + g, c = n0 + 8 * n + 2 * j + e;
+          if (r < rows && c < nk) keys[(int64_t)r * nk + c] = order_key(acc[m][n][e] * scale);
+        }
   }
   __syncthreads();
 
-  for (int r = warp; r < rows; r += kSelThreads / 32) {
-    uint64_t* kr = keys + (int64_t)r * p.nk;
-    const uint64_t forced = ~0ull;                  // above every score's key
-    const int lo_keep = p.keep_first, hi_keep = p.nk - p.keep_last;
-    uint64_t best = 0;
-    for (int i = lane; i < p.nk; i += 32) best = max(best, kr[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = max(best, (uint64_t)__shfl_xor_sync(0xffffffffu, best, o));
+  const int topk = min(p.topk, nk), lo_keep = p.keep_first, hi_keep = nk - p.keep_last;
+  for (int r = warp; r < rows; r += kSelWarps) {
+    uint64_t* kr = keys + (int64_t)r * nk;
+    uint32_t* hs = hist[warp];
+    // Keys kept by position get the highest key; under a margin, keys below the floor the lowest (0, which no
+    // score has), and are never chosen.  same: the bits in which all keys agree.
+    const uint64_t forced = ~0ull;
     uint64_t floor_key = 0;
-    if (p.margin < INFINITY && p.nk > 0) {
+    if (p.margin < INFINITY && nk > 0) {
+      uint64_t best = 0;
+      for (int i = lane; i < nk; i += 32) best = max(best, kr[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) best = max(best, (uint64_t)__shfl_xor_sync(0xffffffffu, best, o));
       const int64_t b = (best >> 63) ? (int64_t)(best & 0x7fffffffffffffffull) : (int64_t)~best;
       floor_key = order_key(__longlong_as_double(b) - p.margin);
     }
-    __syncwarp();
-    for (int i = lane; i < p.nk; i += 32) {
-      if (i < lo_keep || i >= hi_keep) kr[i] = forced;
-      else if (kr[i] < floor_key) kr[i] = 0;         // dropped: below every key that stays
+    uint64_t all_and = ~0ull, all_or = 0;
+    for (int i = lane; i < nk; i += 32) {
+      uint64_t k = kr[i];
+      if (i < lo_keep || i >= hi_keep) kr[i] = k = forced;
+      else if (k < floor_key) kr[i] = k = 0;
+      all_and &= k;
+      all_or |= k;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      all_and &= __shfl_xor_sync(0xffffffffu, all_and, o);
+      all_or |= __shfl_xor_sync(0xffffffffu, all_or, o);
     }
     __syncwarp();
-    // the topk-th largest key, 8 bits at a time: `prefix` holds the bits found, `want` the rank inside them
-    const int topk = min(p.topk, p.nk);
-    uint64_t prefix = 0;
-    int want = topk;                                // 1-based rank among keys that match the prefix
-    for (int shift = 56; shift >= 0 && topk > 0; shift -= 8) {
-      for (int i = lane; i < 256; i += 32) hist[warp][i] = 0;
+    // the topk-th largest key: `prefix` holds the bits found, `want` the 1-based rank among the keys that match it
+    const uint64_t differ = all_and ^ all_or;
+    int shift = differ ? 64 - __clzll(differ) : 0;   // bits below `shift` are still open
+    uint64_t prefix = shift == 64 ? 0ull : all_and >> shift << shift;
+    int want = topk;
+    while (shift > 0 && topk > 0) {
+      const int bits = min(8, shift);
+      const uint64_t hi = shift == 64 ? 0ull : ~0ull << shift;
+      shift -= bits;
+      for (int i = lane; i < 256; i += 32) hs[i] = 0;
       __syncwarp();
-      const uint64_t himask = shift == 56 ? 0ull : (~0ull << (shift + 8));
-      for (int i = lane; i < p.nk; i += 32)
-        if ((kr[i] & himask) == (prefix & himask)) atomicAdd(&hist[warp][(kr[i] >> shift) & 255], 1u);
+      for (int i = lane; i < nk; i += 32) {
+        const uint64_t k = kr[i];
+        if ((k & hi) == prefix) atomicAdd(&hs[(uint32_t)(k >> shift) & ((1u << bits) - 1u)], 1u);
+      }
       __syncwarp();
-      // lane l holds bins 255-8l .. 248-8l (descending); find the bin where the running count reaches want
-      uint32_t mine = 0;
-      for (int e = 0; e < 8; ++e) mine += hist[warp][255 - 8 * lane - e];
+      // lane l holds bins 255-8l .. 248-8l; the bin in which the running count reaches `want`
+      uint32_t c[8], mine = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mine += c[e] = hs[255 - 8 * lane - e];
       uint32_t run = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t u = __shfl_up_sync(0xffffffffu, run, o);
         if (lane >= o) run += u;
       }
-      const uint32_t hit = __ballot_sync(0xffffffffu, run >= (uint32_t)want);
-      const int src = __ffs(hit) - 1;
-      uint32_t before = run - mine;
-      int bin = 0, left = 0;
-      if (lane == src) {
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t c = hist[warp][255 - 8 * lane - e];
-          if (before + c >= (uint32_t)want) { bin = 255 - 8 * lane - e; left = want - (int)before; break; }
-          before += c;
-        }
+      const int src = __ffs(__ballot_sync(0xffffffffu, run >= (uint32_t)want)) - 1;
+      uint32_t before = run - mine, size = 0;
+      int bin = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (size == 0 && before + c[e] >= (uint32_t)want) { bin = 255 - 8 * lane - e; size = c[e]; }
+        else if (size == 0) before += c[e];
       }
       bin = __shfl_sync(0xffffffffu, bin, src);
-      want = __shfl_sync(0xffffffffu, left, src);
+      want -= (int)__shfl_sync(0xffffffffu, before, src);
+      size = __shfl_sync(0xffffffffu, size, src);
       prefix |= (uint64_t)bin << shift;
       __syncwarp();
+      if (size == (uint32_t)want) break;             // every key with this prefix is wanted: no need to tell them apart
     }
-    // chosen: key > prefix, or the first `want` equal to it; key 0 is never chosen (dropped by the margin)
+    // chosen: the prefix and above; where keys equal to it are left over (shift 0), the first `want` of those
     int32_t* out = idx + ((int64_t)h * p.nq + q0 + r) * p.topk;
+    const uint64_t open = shift == 64 ? 0ull : ~0ull << shift;
     int n = 0, eq = 0;
-    for (int i0 = 0; i0 < p.nk && topk > 0; i0 += 32) {
+    for (int i0 = 0; i0 < nk && topk > 0; i0 += 32) {
       const int i = i0 + lane;
-      const uint64_t k = i < p.nk ? kr[i] : 0;
-      const bool same = i < p.nk && k == prefix;
+      const uint64_t k = i < nk ? kr[i] : 0, kp = k & open;
+      const bool same = i < nk && kp == prefix;
       const uint32_t below = (1u << lane) - 1u;
       const uint32_t em = __ballot_sync(0xffffffffu, same);
-      const bool take = i < p.nk && k != 0 && (k > prefix || (same && eq + __popc(em & below) < want));
+      const bool take = i < nk && k != 0 && (kp > prefix || (same && eq + __popc(em & below) < want));
       const uint32_t tm = __ballot_sync(0xffffffffu, take);
       if (take) out[n + __popc(tm & below)] = i;
       n += __popc(tm);
@@ -402,41 +482,40 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const dt_sele
   }
 }
 
-size_t select_smem(int rows, int D, int nk) {
-  return ((size_t)rows * D + (size_t)kSelTile * (D + kSelPad) + (size_t)rows * nk) * 8;
+size_t select_smem(int R, int D, int nk) {
+  return ((size_t)(R > 8 ? 16 : 8) * select_ldq(D) + (size_t)R * nk) * 8;
 }
 
-template <int ROWS>
-int select_launch(const dt_select_params& p, const float* qm, const float* km, int32_t* idx, int32_t* count,
+template <int MT>
+int select_launch(const dt_select_params& p, const float* qm, const float* km, int32_t* idx, int32_t* count, int R,
                   cudaStream_t st) {
-  const size_t smem = select_smem(ROWS, p.D, p.nk);
-  if (cudaFuncSetAttribute(block_select_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+  const size_t smem = select_smem(R, p.D, p.nk);
+  if (cudaFuncSetAttribute(block_select_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return DT_ERR_CUDA;
-  const int qtiles = cdiv(p.nq, ROWS);
-  block_select_kernel<ROWS><<<(unsigned)(p.H * qtiles), kSelThreads, smem, st>>>(p, qm, km, idx, count, qtiles);
+  const int qtiles = cdiv(p.nq, R);
+  block_select_kernel<MT><<<(unsigned)(p.H * qtiles), kSelThreads, smem, st>>>(p, qm, km, idx, count, qtiles, R);
   return launched();
 }
 
 }  // namespace
 
 int launch_rope_table(const RopeTableArgs& a, cudaStream_t stream) {
-  const int64_t n = (int64_t)a.S * ((a.pairs + 1) / 2);
-  const int64_t grid = (n + 255) / 256;
-  rope_table_kernel<<<(unsigned)(grid < (1 << 30) ? grid : (1 << 30)), 256, 0, stream>>>(a);
+  rope_table_kernel<<<(unsigned)cdiv(a.S, kRopeTokens), kRopeThreads, 0, stream>>>(a);
   return launched();
 }
 
 int launch_qk_norm_rope(NormRopeArgs a, int sms, cudaStream_t stream) {
   const dt_norm_rope_params& p = a.p;
-  const int tiles = cdiv(p.S, 128), heads = p.H + 2 * p.Hkv;
-  // heads a CTA walks with one read of the rotation: as many as still leave every SM a few CTAs
-  int64_t per = (int64_t)tiles * heads / (4 * sms);
-  a.heads_per_cta = (int)(per < 1 ? 1 : (per > 8 ? 8 : per));
-  const dim3 grid(tiles, cdiv(heads, a.heads_per_cta));
-  a.store[0] = a.Q != nullptr;
-  a.store[1] = a.K != nullptr;
-  a.store[2] = a.V != nullptr;
+  const int64_t tiles = cdiv(p.S, 128);
+  const int heads = p.H + 2 * p.Hkv;
+  // warps per head and tile: one, or more while the CTAs are fewer than two per SM
+  a.wt = 1;
+  while (a.wt < kNormWarps && tiles * cdiv(heads * a.wt, kNormWarps) < 2 * sms) a.wt *= 2;
+  a.groups = cdiv(heads * a.wt, kNormWarps);
+  a.inv_d = 1.f / (float)p.D;
+  if (tiles * a.groups >= (int64_t)1 << 31) return DT_ERR_INVALID;
+  const unsigned grid = (unsigned)(tiles * a.groups);
   if (p.in_type == DT_TYPE_BF16) norm_rope_dispatch<__nv_bfloat16, __nv_bfloat16>(a, grid, stream);
   else if (p.in_type == DT_TYPE_F16 && p.out_type == DT_TYPE_F16) norm_rope_dispatch<__half, __half>(a, grid, stream);
   else if (p.in_type == DT_TYPE_F16) norm_rope_dispatch<__half, __nv_bfloat16>(a, grid, stream);
@@ -447,11 +526,13 @@ int launch_qk_norm_rope(NormRopeArgs a, int sms, cudaStream_t stream) {
 
 int launch_block_select(const dt_select_params& p, const float* q_mean, const float* k_mean, int32_t* idx,
                         int32_t* count, cudaStream_t stream) {
-  // rows per CTA: as many as their keys fit in shared memory (the K tile is then staged for more rows)
-  constexpr size_t kMax = 200 * 1024;
-  if (p.nq > 8 && select_smem(16, p.D, p.nk) <= kMax) return select_launch<16>(p, q_mean, k_mean, idx, count, stream);
-  if (p.nq > 2 && select_smem(8, p.D, p.nk) <= kMax) return select_launch<8>(p, q_mean, k_mean, idx, count, stream);
-  return select_launch<1>(p, q_mean, k_mean, idx, count, stream);
+  // Query blocks per CTA: as many as there are, up to 16, while the keys of
+  // the rows leave room for a second CTA on the SM (one scores while the other
+  // selects); long rows take what one CTA may have.
+  int R = 16;
+  while (R > 1 && (R / 2 >= p.nq || select_smem(R, p.D, p.nk) > 100 * 1024)) R /= 2;
+  return R > 8 ? select_launch<2>(p, q_mean, k_mean, idx, count, R, stream)
+               : select_launch<1>(p, q_mean, k_mean, idx, count, R, stream);
 }
 
 }  // namespace dt

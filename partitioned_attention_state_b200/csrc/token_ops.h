@@ -15,7 +15,7 @@ struct RopeTableArgs {
   const int32_t* pos;
   float* table;
   int S, pairs;
-  double turns[kMaxPairs];                  // turns per unit of position: base^(-2j/dim) / (2 pi)
+  uint64_t turns[kMaxPairs];                // turns per unit of position, base^(-2j/dim) / (2 pi), as a 64-bit fraction
   uint8_t axis[kMaxPairs];
 };
 int launch_rope_table(const RopeTableArgs& a, cudaStream_t stream);
@@ -26,8 +26,8 @@ struct NormRopeArgs {
   const float *wq, *wk, *table;
   float *q_mean, *k_mean;
   dt_norm_rope_params p;
-  int heads_per_cta;                        // set by the launcher, like store
-  int store[3];                             // Q, K, V are written (else means alone)
+  int wt, groups;                           // warps per head and tile, CTAs per tile (set by the launcher, like inv_d)
+  float inv_d;
 };
 int launch_qk_norm_rope(NormRopeArgs a, int sms, cudaStream_t stream);
 
