@@ -18,9 +18,13 @@
 // their states (m, l, unnormalised O) through distributed shared memory.
 //
 // Per CTA, 16 warps (4 warpgroups, registers rebalanced with setmaxnreg):
-//   warps 0-7   softmax: two warps per SM sub-partition, each owning 16 rows of
-//               the tile (16-lane TMEM accesses; a thread holds 2 rows x 32
-//               columns); P is written back over S in TMEM as 16-bit values
+//   warps 0-7   softmax: two sets of four warps that take alternate tiles, a row
+//               per thread; P is written back over S in TMEM as 16-bit values.
+//               One set's exponentials (1,024 clk of the exponential unit per
+//               tile) run while the other hands its tile on, loads the next S and
+//               takes its maxima.  Both scale by one reference maximum per row,
+//               handed from set to set in shared memory, so that O stays a single
+//               accumulator; a row's sum is kept by each set and added at the end
 //   warps 8-11  epilogue: O (TMEM) -> registers, TMEM released, normalised rows
 //               and LSEs to memory, under the next item's tiles
 //   warp 12     tcgen05.mma S = Q K^T; TMEM alloc/free
@@ -58,7 +62,7 @@ constexpr int kWarpEpi = 8, kWarpMma = 12, kWarpTmaK = 13, kWarpTmaV = 14, kWarp
 // Registers per thread at launch (the build checks that ptxas chose them) and
 // the per-warpgroup split, which must fit the launch pool.
 constexpr int kLaunchRegs = 128;
-constexpr int kRegsSoftmax = 128, kRegsEpilogue = 192, kRegsOther = 64;
+constexpr int kRegsSoftmax = 184, kRegsEpilogue = 96, kRegsOther = 48;
 static_assert(128 * (2 * kRegsSoftmax + kRegsEpilogue + kRegsOther) <= kThreads * kLaunchRegs, "register split");
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 constexpr int kMaxDevices = 64;
@@ -88,22 +92,15 @@ struct Cfg {
   static constexpr int bQFull = 0, bQEmpty = bQFull + kNQ, bKFull = bQEmpty + kNQ, bVFull = bKFull + kNK,
                        bKEmpty = bVFull + kNV, bVEmpty = bKEmpty + kNK, bSFull = bVEmpty + kNV,
                        bPFull = bSFull + kNS, bPVDone = bPFull + kNS, bOFull = bPVDone + kNS, bOFree = bOFull + 1,
-                       bStFull = bOFree + 1, bStFree = bStFull + 2, bDrain = bStFree + 2, bDrainPV = bDrain + 1,
-                       kNumBars = bDrainPV + 1;
-  static constexpr int kStatsBytes = 2 * 2 * 128 * 4;
+                       bStFull = bOFree + 1, bStFree = bStFull + 1, bTok = bStFree + 1, bDrain = bTok + 8,
+                       bDrainPV = bDrain + 1, kNumBars = bDrainPV + 1;
+  // per row: reference maximum, and each set's (maximum, sum) of the item
+  static constexpr int kStatsBytes = 5 * 128 * 4;
   static constexpr int kSmem = kTileBytes * (kNQ + kNK + kNV) + kStatsBytes + kNumBars * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
   // a split item's partial O ([128][DP] fp32) reuses the K ring, drained by then
   static_assert(kNK * kTileBytes >= 128 * DP * 4, "partial O fits the K ring");
 };
-
-// Columns c_j = 8*(j/2) + cq + (j%2), j = 0..31, that a softmax thread holds:
-// how many of them are below x (they increase in j).
-__device__ __forceinline__ int cols_below(int x, int cq) {
-  const int y = x - cq;
-  return imin(imax((y + 7) >> 3, 0), 16) + imin(imax((y + 6) >> 3, 0), 16);
-}
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : ((1u << n) - 1u); }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
                                           uint64_t limit) {
@@ -130,9 +127,15 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, int b_mn) {
 // The list's length and its first entries are loaded an item ahead, and every
 // other entry a tile ahead: a load from L2 costs as much as a third of a tile,
 // and two one after another at every item cost each role 1-2 us.
+// Volatile, or the compiler moves the load down to the value's use.
+__device__ __forceinline__ int ld_ahead(const int32_t* a) {
+  int v;
+  asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
+}
 struct Item { int h, q0, rows, n, t0, t1; };
 __device__ __forceinline__ int load_count(const SparseParams& p, int item) {
-  return p.count && item < p.H * p.nqb ? __ldg(p.count + item) : p.cap;
+  return p.count && item < p.H * p.nqb ? ld_ahead(p.count + item) : p.cap;
 }
 __device__ __forceinline__ Item make_item(const SparseParams& p, int item, int rank, int count) {
   Item it;
@@ -152,8 +155,8 @@ __device__ __forceinline__ Entries load_entries(const SparseParams& p, int item,
   const int i = t * p.per_tile;
   if (item < p.H * p.nqb && i < p.cap) {
     const int32_t* l = p.idx + (int64_t)item * p.cap + i;
-    e.a = __ldg(l);
-    if (p.per_tile == 2 && i + 1 < p.cap) e.b = __ldg(l + 1);
+    e.a = ld_ahead(l);
+    if (p.per_tile == 2 && i + 1 < p.cap) e.b = ld_ahead(l + 1);
   }
   return e;
 }
@@ -232,9 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + C::kNQ * C::kTileBytes;
   uint8_t* sV = sK + C::kNK * C::kTileBytes;
-  float* stat_m = reinterpret_cast<float*>(sV + C::kNV * C::kTileBytes);      // [2][128]
-  float* stat_l = stat_m + 256;                                              // [2][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stat_l + 256);
+  float* stat_m = reinterpret_cast<float*>(sV + C::kNV * C::kTileBytes);      // [2 sets][128]
+  float* stat_l = stat_m + 256;                                              // [2 sets][128]
+  float* s_ref = stat_l + 256;                                               // [128]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_ref + 128);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -247,11 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
   if (warp == kWarpTmaK && lane == 0) {
     for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bars[i], 1);
     // every thread of the arriving role arrives (no single-lane branches)
-    for (int i = 0; i < C::kNS; ++i) mbar_init(&bars[C::bPFull + i], 8 * 32);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[C::bStFull + i], 8 * 32);
-      mbar_init(&bars[C::bStFree + i], 4 * 32);
-    }
+    for (int i = 0; i < C::kNS; ++i) mbar_init(&bars[C::bPFull + i], 4 * 32);
+    for (int i = 0; i < 8; ++i) mbar_init(&bars[C::bTok + i], 32);
+    mbar_init(&bars[C::bStFull], 8 * 32);
+    mbar_init(&bars[C::bStFree], 4 * 32);
     mbar_init(&bars[C::bOFree], 4 * 32);
     *abort_flag = 0;
     fence_barrier_init();
@@ -345,58 +348,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       __syncwarp();
     } else if (warp == kWarpMma) {
       // ---------------------------------------------------------- S = Q K^T
-      if (lane == 0) {
-        constexpr uint32_t idesc = idesc16<F16>(128, 128, 0);
-        const uint32_t aK = smem_u32(sK);
-        uint32_t g = 0, nq = 0;
-        bool ok = true;
-        int count = load_count(p, item0);
-        for (int item = item0; item < items && ok; item += istep) {
-          const Item it = make_item(p, item, rank, count);
-          count = load_count(p, item + istep);
-          if (it.t0 == it.t1) continue;
-          const uint32_t qb = nq % C::kNQ;
-          const uint32_t aQ = smem_u32(sQ) + qb * C::kTileBytes;
-          if (!mbar_wait(&bars[C::bQFull + qb], (nq / C::kNQ) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim)) break;
-          ++nq;
-          for (int t = it.t0; t < it.t1; ++t, ++g) {
-            const uint32_t st = g % C::kNK, sb = g % C::kNS;
-            if (!mbar_wait(&bars[C::bKFull + st], (g / C::kNK) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim)) {
-              ok = false;
-              break;
-            }
-            // S buffer sb held P(g-3): its P V (issued by warp 15) must be done
-            if (g >= (uint32_t)C::kNS &&
-                !mbar_wait(&bars[C::bPVDone + sb], (g / C::kNS - 1) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+      // The MMA warps run their loops whole and elect a lane for each tile's
+      // instructions, so that descriptors stay in uniform registers: issued by
+      // one lane of a divergent loop an MMA took ~115 clk, and 8 of them nearly a
+      // whole tile's time.
+      constexpr uint32_t idesc = idesc16<F16>(128, 128, 0);
+      const uint64_t qd0 = smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+      const uint64_t kd0 = smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
+      const uint64_t qt0 = smem_desc(smem_u32(sQ) + C::kN64 * C::kBlk, 16, 256, kSwizzle32B);
+      const uint64_t kt0 = smem_desc(smem_u32(sK) + C::kN64 * C::kBlk, 16, 256, kSwizzle32B);
+      uint32_t g = 0, nq = 0;
+      bool ok = true;
+      int count = load_count(p, item0);
+      for (int item = item0; item < items && ok; item += istep) {
+        const Item it = make_item(p, item, rank, count);
+        count = load_count(p, item + istep);
+        if (it.t0 == it.t1) continue;
+        const uint32_t qb = nq % C::kNQ;
+        ok = warp_wait(&bars[C::bQFull + qb], (nq / C::kNQ) & 1, abort_flag, p.status, lim);
+        ++nq;
+        for (int t = it.t0; t < it.t1 && ok; ++t, ++g) {
+          const uint32_t st = g % C::kNK, sb = g % C::kNS;
+          // K has arrived, and S buffer sb, which held P(g-3), is free: its P V (issued by warp 15) is done
+          ok = warp_wait(&bars[C::bKFull + st], (g / C::kNK) & 1, abort_flag, p.status, lim) &&
+               (g < (uint32_t)C::kNS ||
+                warp_wait(&bars[C::bPVDone + sb], (g / C::kNS - 1) & 1, abort_flag, p.status, lim));
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
             const uint32_t dS = tmem + C::kColS + sb * 128;
-            const uint32_t kb = aK + st * C::kTileBytes;
-            uint32_t acc = 0u;
-#pragma unroll 1
-            for (int blk = 0; blk < C::kN64; ++blk) {
-              uint64_t qd = smem_desc(aQ + blk * C::kBlk, 16, 1024, kSwizzle128B);
-              uint64_t kd = smem_desc(kb + blk * C::kBlk, 16, 1024, kSwizzle128B);
+            const uint64_t qd = qd0 + qb * (C::kTileBytes >> 4), kd = kd0 + st * (C::kTileBytes >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {             // 16 head-dim columns (32 bytes of a row) per MMA
-                mma_ss(dS, qd, kd, idesc, acc);
-                acc = 1u;
-                qd += 32 >> 4;
-                kd += 32 >> 4;
-              }
-            }
-            if (C::kTail) {
-              const uint32_t off = C::kN64 * C::kBlk;
-              mma_ss(dS, smem_desc(aQ + off, 16, 256, kSwizzle32B), smem_desc(kb + off, 16, 256, kSwizzle32B), idesc, 1u);
-            }
+            for (int blk = 0; blk < C::kN64; ++blk)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)               // 16 head-dim columns (32 bytes of a row) per MMA
+                mma_ss(dS, qd + (blk * C::kBlk + kk * 32 >> 4), kd + (blk * C::kBlk + kk * 32 >> 4), idesc,
+                       blk + kk > 0 ? 1u : 0u);
+            if (C::kTail)
+              mma_ss(dS, qt0 + qb * (C::kTileBytes >> 4), kt0 + st * (C::kTileBytes >> 4), idesc, 1u);
             mma_commit(&bars[C::bSFull + sb]);
             mma_commit(&bars[C::bKEmpty + st]);
+            if (t == it.t1 - 1) mma_commit(&bars[C::bQEmpty + qb]);
           }
-          mma_commit(&bars[C::bQEmpty + qb]);
+          __syncwarp();
         }
-        // all MMAs this thread issued complete before tensor memory is freed
+      }
+      // all MMAs that this warp issued complete before tensor memory is freed
+      if (elect_one()) {
         mma_commit(&bars[C::bDrain]);
         volatile int never = 0;
         mbar_wait(&bars[C::bDrain], 0, &never, p.status, DT_ERR_TIMEOUT, kDrainLimitNs);
@@ -404,48 +402,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       __syncwarp();
     } else if (warp == kWarpMmaPV) {
       // ---------------------------------------------------------- O += P V
-      if (lane == 0) {
-        constexpr uint32_t idesc_pv = idesc16<F16>(128, 64 * C::kN64, 1);
-        constexpr uint32_t idesc_pvt = idesc16<F16>(128, 16, 1);
-        const uint32_t aV = smem_u32(sV);
-        uint32_t g = 0, nq = 0;
-        bool ok = true;
-        int count = load_count(p, item0);
-        for (int item = item0; item < items && ok; item += istep) {
-          const Item it = make_item(p, item, rank, count);
-          count = load_count(p, item + istep);
-          if (it.t0 == it.t1) continue;
-          for (int t = it.t0; t < it.t1 && ok; ++t, ++g) {
-            const uint32_t sb = g % C::kNS, st = g % C::kNV;
-            ok = mbar_wait(&bars[C::bPFull + sb], (g / C::kNS) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim) &&
-                 (t > it.t0 || nq == 0 ||
-                  mbar_wait(&bars[C::bOFree], (nq - 1) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim)) &&
-                 mbar_wait(&bars[C::bVFull + st], (g / C::kNV) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t aP = tmem + C::kColS + sb * 128;
-            const uint32_t vb = aV + st * C::kTileBytes;
-            // 16 keys per MMA: descriptors advance by 16 V rows.  A tile that
-            // holds one 64-key block ends after 4.
-            const int kn = p.per_tile == 2 && 2 * t + 1 >= it.n ? 4 : 8;
-            uint64_t vd = smem_desc(vb, C::kBlk, 1024, kSwizzle128B);
-            uint64_t vdt = smem_desc(vb + C::kN64 * C::kBlk, C::kTailBytes, 256, kSwizzle32B);
-            uint32_t acc = t > it.t0 ? 1u : 0u;
-#pragma unroll 1
-            for (int kk = 0; kk < kn; ++kk) {
-              mma_ts(tmem + C::kColO, aP, vd, idesc_pv, acc);
-              if (C::kTail) mma_ts(tmem + C::kColO + 64 * C::kN64, aP, vdt, idesc_pvt, acc);
-              acc = 1u;
-              aP += 8;
-              vd += 2048 >> 4;
-              vdt += 512 >> 4;
+      constexpr uint32_t idesc_pv = idesc16<F16>(128, 64 * C::kN64, 1);
+      constexpr uint32_t idesc_pvt = idesc16<F16>(128, 16, 1);
+      const uint64_t vd0 = smem_desc(smem_u32(sV), C::kBlk, 1024, kSwizzle128B);
+      const uint64_t vt0 = smem_desc(smem_u32(sV) + C::kN64 * C::kBlk, C::kTailBytes, 256, kSwizzle32B);
+      uint32_t g = 0, nq = 0;
+      bool ok = true;
+      int count = load_count(p, item0);
+      for (int item = item0; item < items && ok; item += istep) {
+        const Item it = make_item(p, item, rank, count);
+        count = load_count(p, item + istep);
+        if (it.t0 == it.t1) continue;
+        for (int t = it.t0; t < it.t1 && ok; ++t, ++g) {
+          const uint32_t sb = g % C::kNS, st = g % C::kNV;
+          ok = warp_wait(&bars[C::bVFull + st], (g / C::kNV) & 1, abort_flag, p.status, lim) &&
+               (t > it.t0 || nq == 0 || warp_wait(&bars[C::bOFree], (nq - 1) & 1, abort_flag, p.status, lim)) &&
+               warp_wait(&bars[C::bPFull + sb], (g / C::kNS) & 1, abort_flag, p.status, lim);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t aP = tmem + C::kColS + sb * 128;
+            const uint64_t vd = vd0 + st * (C::kTileBytes >> 4), vdt = vt0 + st * (C::kTileBytes >> 4);
+            const uint32_t acc = t > it.t0 ? 1u : 0u;
+            // 16 keys per MMA: descriptors advance by 16 V rows
+            auto pv = [&](int kk) {
+              mma_ts(tmem + C::kColO, aP + 8 * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1u : acc);
+              if (C::kTail)
+                mma_ts(tmem + C::kColO + 64 * C::kN64, aP + 8 * kk, vdt + kk * (512 >> 4), idesc_pvt, kk > 0 ? 1u : acc);
+            };
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) pv(kk);
+            if (p.per_tile == 1 || 2 * t + 1 < it.n) {      // a tile that holds one 64-key block ends here
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk) pv(kk);
             }
             mma_commit(&bars[C::bVEmpty + st]);
             mma_commit(&bars[C::bPVDone + sb]);
             if (t == it.t1 - 1) mma_commit(&bars[C::bOFull]);
           }
-          ++nq;
+          __syncwarp();
         }
+        ++nq;
+      }
+      if (elect_one()) {
         mma_commit(&bars[C::bDrainPV]);
         volatile int never = 0;
         mbar_wait(&bars[C::bDrainPV], 0, &never, p.status, DT_ERR_TIMEOUT, kDrainLimitNs);
@@ -455,141 +454,133 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
   } else if (warp < kWarpEpi) {
     regs_set<kLaunchRegs, kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
-    // Warp w owns tile rows rbase .. rbase+15; thread t holds rows ra = rbase +
-    // t/4 and rb = ra + 8 at columns 8i + 2(t%4) + {0,1}, i = 0..15.
-    const int rbase = (warp & 3) * 32 + (warp >> 2) * 16;
-    const int ra = rbase + (lane >> 2), rb = ra + 8;
-    const int cq = 2 * (lane & 3);
-    const uint32_t lane_base = static_cast<uint32_t>(rbase) << 16;
+    // Set `set` takes the tiles g = set, set + 2, ... (counted over the CTA's
+    // items); thread = tile row.  Tile g's reference maximum follows from tile
+    // g-1's, which the other set's warp of the same rows hands over through
+    // s_ref and the token barrier: the order of the tiles, and with it the
+    // result, is that of one set.
+    const int set = warp >> 2, pair = warp & 3;
+    const int r = pair * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(pair * 32) << 16;
     const float sl2 = p.scale_log2;
-    uint32_t g = 0, nq = 0;
+    uint64_t* tok_in = &bars[C::bTok + 2 * pair + (set ^ 1)];
+    uint64_t* tok_out = &bars[C::bTok + 2 * pair + set];
+    uint32_t g0 = 0, nq = 0;                       // first tile of the item, items done
     int count = load_count(p, item0);
-    Entries first = load_entries(p, item0, make_item(p, item0, rank, count).t0);
+    Entries first;
+    {
+      const Item it = make_item(p, item0, rank, count);
+      first = load_entries(p, item0, it.t0 + set);
+    }
     for (int item = item0; item < items; item += istep) {
       const Item it = make_item(p, item, rank, count);
+      const int nt = it.t1 - it.t0;
+      const int i0 = (g0 & 1) == (uint32_t)set ? 0 : 1;                  // this set's first tile of the item
       Entries nxt = first;
       count = load_count(p, item + istep);
-      first = load_entries(p, item + istep, 0);
-      if (it.t0 == it.t1) continue;
-      const bool idle = rbase >= it.rows;          // none of this warp's rows exist: hand the tiles on
-      float ma = neg_inf(), mb = neg_inf();         // running max (log2 units)
-      uint64_t la[2] = {0ull, 0ull}, lb[2] = {0ull, 0ull};      // packed pairs of partial row sums
-      for (int t = it.t0; t < it.t1; ++t, ++g) {
-        const uint32_t sb = g % C::kNS;
-        const Halves hv = tile_halves(p, it, t, nxt);
-        if (t + 1 < it.t1) nxt = load_entries(p, item, t + 1);
+      first = load_entries(p, item + istep, ((g0 + nt) & 1) == (uint32_t)set ? 0 : 1);
+      if (nt == 0) continue;
+      const bool idle = pair * 32 >= it.rows;      // none of this warp's rows exist: hand the tiles on
+      float m = neg_inf();                          // reference (log2 units) that l stands on
+      uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};    // packed pairs of partial row sums
+      for (int i = i0; i < nt; i += 2) {
+        const uint32_t g = g0 + i, sb = g % C::kNS;
+        const Halves hv = tile_halves(p, it, it.t0 + i, nxt);
+        if (i + 2 < nt) nxt = load_entries(p, item, it.t0 + i + 2);
         if (!warp_wait(&bars[C::bSFull + sb], (g / C::kNS) & 1, abort_flag, p.status, lim)) goto sm_done;
         if (idle) {
+          if (g > 0 && !warp_wait(tok_in, ((g - 1) >> 1) & 1, abort_flag, p.status, lim)) goto sm_done;
+          mbar_arrive(tok_out);
           mbar_arrive(&bars[C::bPFull + sb]);
           continue;
         }
         tc_fence_after();
         const uint32_t sc = tmem + lane_base + C::kColS + sb * 128;
-        uint32_t sr[64];
-        tmem_ld_16x256b_x8(sc, sr);
-        tmem_ld_16x256b_x8(sc + 64, sr + 32);
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) tmem_ld32(sc + c, sr + c);
         tmem_wait_ld();
         const int v0 = p.Sk - hv.r0, v1 = hv.r1 < 0 ? 0 : p.Sk - hv.r1;      // keys of each half
         if (v0 < 64 || v1 < 64) {
-          // kept columns as a bit mask over this thread's 32, one test per
-          // element: compact code for the rare tile.  Assigned, not added: the
-          // logits there may be anything.
-          const uint32_t keep = low_bits(cols_below(imin(v0, 64), cq)) |
-                                (low_bits(cols_below(64 + imin(v1, 64), cq)) & ~low_bits(cols_below(64, cq)));
+          // assigned, not added: the logits there may be anything
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (!(keep & (1u << (2 * (e >> 2) + (e & 1))))) sr[e] = f2u(neg_inf());
+          for (int e = 0; e < 128; ++e)
+            if (!((e & 63) < (e < 64 ? v0 : v1))) sr[e] = f2u(neg_inf());
         }
-        // row maxima: two chains per row, then across the 4 threads of a row
-        float xa0 = fmaxf(u2f(sr[0]), u2f(sr[1])), xa1 = fmaxf(u2f(sr[4]), u2f(sr[5]));
-        float xb0 = fmaxf(u2f(sr[2]), u2f(sr[3])), xb1 = fmaxf(u2f(sr[6]), u2f(sr[7]));
+        float x0 = max3f(u2f(sr[0]), u2f(sr[1]), u2f(sr[2])), x1 = max3f(u2f(sr[3]), u2f(sr[4]), u2f(sr[5]));
+        float x2 = max3f(u2f(sr[6]), u2f(sr[7]), u2f(sr[8])), x3 = max3f(u2f(sr[9]), u2f(sr[10]), u2f(sr[11]));
 #pragma unroll
-        for (int r4 = 2; r4 < 16; r4 += 2) {
-          xa0 = max3f(xa0, u2f(sr[4 * r4]), u2f(sr[4 * r4 + 1]));
-          xa1 = max3f(xa1, u2f(sr[4 * r4 + 4]), u2f(sr[4 * r4 + 5]));
-          xb0 = max3f(xb0, u2f(sr[4 * r4 + 2]), u2f(sr[4 * r4 + 3]));
-          xb1 = max3f(xb1, u2f(sr[4 * r4 + 6]), u2f(sr[4 * r4 + 7]));
+        for (int e = 12; e < 124; e += 8) {
+          x0 = max3f(x0, u2f(sr[e]), u2f(sr[e + 1]));
+          x1 = max3f(x1, u2f(sr[e + 2]), u2f(sr[e + 3]));
+          x2 = max3f(x2, u2f(sr[e + 4]), u2f(sr[e + 5]));
+          x3 = max3f(x3, u2f(sr[e + 6]), u2f(sr[e + 7]));
         }
-        float mxa = fmaxf(xa0, xa1), mxb = fmaxf(xb0, xb1);
-        mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
-        mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-        mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
-        mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-        const float mxa2 = mxa * sl2, mxb2 = mxb * sl2;
-        const bool first = t == it.t0;
-        const float na = first ? mxa2 : ((mxa2 > ma + kRescaleThreshold) ? mxa2 : ma);
-        const float nb = first ? mxb2 : ((mxb2 > mb + kRescaleThreshold) ? mxb2 : mb);
-        // a row that has seen only masked keys (max -inf) has O = 0 and l = 0:
-        // it takes the new reference without a rescale
-        const bool resa = !first && (na != ma) && (ma != neg_inf());
-        const bool resb = !first && (nb != mb) && (mb != neg_inf());
-        if (__any_sync(0xffffffffu, resa || resb)) {
+        x0 = max3f(x0, u2f(sr[124]), u2f(sr[125]));
+        x1 = max3f(x1, u2f(sr[126]), u2f(sr[127]));
+        const float mx2 = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * sl2;
+        // the reference after the previous tile, and after this one
+        if (g > 0 && !warp_wait(tok_in, ((g - 1) >> 1) & 1, abort_flag, p.status, lim)) goto sm_done;
+        const float old = i == 0 ? neg_inf() : s_ref[r];
+        const float ref = i == 0 ? mx2 : (mx2 > old + kRescaleThreshold ? mx2 : old);
+        // a row that has seen only masked keys (reference -inf) has O = 0: it takes the new one without a rescale
+        const bool res = ref != old && old != neg_inf();
+        if (__any_sync(0xffffffffu, res)) {
           // O holds the previous tiles' sum: wait for its last P V, then rescale
           if (!warp_wait(&bars[C::bPVDone + (g - 1) % C::kNS], ((g - 1) / C::kNS) & 1, abort_flag, p.status, lim))
             goto sm_done;
           tc_fence_after();
-          const float alpha_a = resa ? ex2(ma - na) : 1.f, alpha_b = resb ? ex2(mb - nb) : 1.f;
+          const float alpha = res ? ex2(old - ref) : 1.f;
           const uint32_t oc = tmem + lane_base + C::kColO;
 #pragma unroll 1
           for (int c0 = 0; c0 < DP; c0 += 16) {
-            uint32_t o[8];
-            tmem_ld_16x256b_x2(oc + c0, o);
+            uint32_t o[16];
+            tmem_ld16(oc + c0, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = f2u(u2f(o[e]) * ((e & 2) ? alpha_b : alpha_a));
-            tmem_st_16x256b_x2(oc + c0, o);
+            for (int e = 0; e < 16; ++e) o[e] = f2u(u2f(o[e]) * alpha);
+            tmem_st16(oc + c0, o);
           }
           tmem_wait_st();
-          const uint64_t aa = pk2(alpha_a, alpha_a), ab = pk2(alpha_b, alpha_b);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) { la[k] = fma2(la[k], aa, 0ull); lb[k] = fma2(lb[k], ab, 0ull); }
         }
-        ma = na; mb = nb;
-        const float mra = (ma == neg_inf()) ? 0.f : ma, mrb = (mb == neg_inf()) ? 0.f : mb;
-        const uint64_t sl2x2 = pk2(sl2, sl2), nma = pk2(-mra, -mra), nmb = pk2(-mrb, -mrb);
-        // exponentials, 8 repetitions (32 P columns) per TMEM store
+        s_ref[r] = ref;
+        mbar_arrive(tok_out);
+        if (m != ref) {                             // l onto the new reference (0 while m is -inf)
+          const float beta = ex2(m - ref);
+          const uint64_t b2 = pk2(beta, beta);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
+          for (int k = 0; k < 4; ++k) l2[k] = mul2(l2[k], b2);
+          m = ref;
+        }
+        const float mr = ref == neg_inf() ? 0.f : ref;
+        const uint64_t sl2x2 = pk2(sl2, sl2), nm = pk2(-mr, -mr);
+        // exponentials, 32 columns (16 P columns) per TMEM store
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
           uint32_t ph[16];
 #pragma unroll
-          for (int r4 = 0; r4 < 8; ++r4) {
-            const int e = 4 * (8 * hf + r4);
-            float x0, x1, x2, x3;
-            upk2(fma2(pk2(u2f(sr[e]), u2f(sr[e + 1])), sl2x2, nma), x0, x1);
-            upk2(fma2(pk2(u2f(sr[e + 2]), u2f(sr[e + 3])), sl2x2, nmb), x2, x3);
-            const float p0 = ex2(x0), p1 = ex2(x1), p2 = ex2(x2), p3 = ex2(x3);
-            la[r4 & 1] = add2(la[r4 & 1], pk2(p0, p1));
-            lb[r4 & 1] = add2(lb[r4 & 1], pk2(p2, p3));
-            ph[2 * r4] = pack16<F16>(p0, p1);
-            ph[2 * r4 + 1] = pack16<F16>(p2, p3);
+          for (int e = 0; e < 32; e += 2) {
+            float a, b;
+            upk2(fma2(pk2(u2f(sr[c + e]), u2f(sr[c + e + 1])), sl2x2, nm), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            l2[(e >> 1) & 3] = add2(l2[(e >> 1) & 3], pk2(a, b));
+            ph[e >> 1] = pack16<F16>(a, b);
           }
-          tmem_st_16x128b_x8(sc + 32 * hf, ph);
+          tmem_st16(sc + c / 2, ph);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bars[C::bPFull + sb]);
       }
-      float sa, sbm;
-      {
-        float u0, u1, w0, w1;
-        upk2(add2(la[0], la[1]), u0, u1);
-        upk2(add2(lb[0], lb[1]), w0, w1);
-        sa = u0 + u1;
-        sbm = w0 + w1;
-      }
-      sa += __shfl_xor_sync(0xffffffffu, sa, 1);
-      sbm += __shfl_xor_sync(0xffffffffu, sbm, 1);
-      sa += __shfl_xor_sync(0xffffffffu, sa, 2);
-      sbm += __shfl_xor_sync(0xffffffffu, sbm, 2);
-      const uint32_t st = nq & 1;
-      if (nq >= 2 && !warp_wait(&bars[C::bStFree + st], ((nq >> 1) - 1) & 1, abort_flag, p.status, lim)) goto sm_done;
-      // the 4 threads of a row hold the same values: all of them write
-      stat_m[st * 128 + ra] = ma;
-      stat_l[st * 128 + ra] = sa;
-      stat_m[st * 128 + rb] = mb;
-      stat_l[st * 128 + rb] = sbm;
-      mbar_arrive(&bars[C::bStFull + st]);
+      float u0, u1;
+      upk2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])), u0, u1);
+      if (nq >= 1 && !warp_wait(&bars[C::bStFree], (nq - 1) & 1, abort_flag, p.status, lim)) goto sm_done;
+      stat_m[set * 128 + r] = m;
+      stat_l[set * 128 + r] = u0 + u1;
+      mbar_arrive(&bars[C::bStFull]);
       ++nq;
+      g0 += nt;
     }
   sm_done:;
   } else {
@@ -616,37 +607,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         }
         continue;
       }
-      const uint32_t st = nq & 1;
-      if (!warp_wait(&bars[C::bStFull + st], (nq >> 1) & 1, abort_flag, p.status, lim)) goto ep_done;
-      const float m = stat_m[st * 128 + r], l = stat_l[st * 128 + r];
-      mbar_arrive(&bars[C::bStFree + st]);
+      if (!warp_wait(&bars[C::bStFull], nq & 1, abort_flag, p.status, lim)) goto ep_done;
+      // references only rise, so O stands on the higher of the sets'; a set that had no tile has (-inf, 0)
+      const float ma = stat_m[r], mb = stat_m[128 + r], la = stat_l[r], lb = stat_l[128 + r];
+      const float m = ma != ma || mb != mb ? ma + mb : fmaxf(ma, mb);
+      const float l = (ma == m ? la : la * ex2(ma - m)) + (mb == m ? lb : lb * ex2(mb - m));
+      if (p.split > 1) {
+        stat_m[r] = m;
+        stat_l[r] = l;
+      }
+      mbar_arrive(&bars[C::bStFree]);
       if (!warp_wait(&bars[C::bOFull], nq & 1, abort_flag, p.status, lim)) goto ep_done;
       tc_fence_after();
-      uint32_t op[DP];
+      // l > 0 unless every listed key is past the end or has a logit of -inf; NaN stays
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float* part = reinterpret_cast<float*>(sK);
 #pragma unroll
-      for (int c0 = 0; c0 < DP; c0 += 16) tmem_ld16p(oaddr + c0, op + c0);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(&bars[C::bOFree]);
-      if (p.split > 1) {
-        float* part = reinterpret_cast<float*>(sK);
-        if (valid)
+      for (int c0 = 0; c0 < DP; c0 += 32) {
+        constexpr int kLast = DP - (DP - 1) / 32 * 32;    // columns of the last step
+        uint32_t op[32];
 #pragma unroll
-          for (int c = 0; c < D; c += 4)
-            *reinterpret_cast<float4*>(part + part_chunk<DP>(r, c / 4)) =
-                make_float4(u2f(op[c]), u2f(op[c + 1]), u2f(op[c + 2]), u2f(op[c + 3]));
-      } else if (valid) {
-        // l > 0 unless every listed key is past the end or has a logit of -inf; NaN stays
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int c = 0; c < D; c += 8) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : u2f(op[c + e]) * inv;
-          store_out8<F16>(p, orow + c, x);
+        for (int c = 0; c < (c0 + 32 <= DP ? 32 : kLast); c += 16) tmem_ld16p(oaddr + c0 + c, op + c);
+        tmem_wait_ld();
+        if (c0 + 32 >= DP) {                              // all of O is read: hand it back
+          tc_fence_before();
+          mbar_arrive(&bars[C::bOFree]);
         }
-        *lrow = l == 0.f ? neg_inf() : (m + lg2(l)) * kLn2;
+        if (!valid) continue;
+#pragma unroll
+        for (int c = 0; c < 32 && c0 + c < D; c += 8) {
+          float x[8];
+          if (p.split > 1) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+              *reinterpret_cast<float4*>(part + part_chunk<DP>(r, (c0 + c + e) / 4)) =
+                  make_float4(u2f(op[c + e]), u2f(op[c + e + 1]), u2f(op[c + e + 2]), u2f(op[c + e + 3]));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : u2f(op[c + e]) * inv;
+            store_out8<F16>(p, orow + c0 + c, x);
+          }
+        }
       }
+      if (p.split == 1 && valid) *lrow = l == 0.f ? neg_inf() : (m + lg2(l)) * kLn2;
       ++nq;
     }
   ep_done:;
