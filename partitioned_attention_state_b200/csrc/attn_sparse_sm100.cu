@@ -102,10 +102,29 @@ struct Cfg {
   static_assert(kNK * kTileBytes >= 128 * DP * 4, "partial O fits the K ring");
 };
 
+// Bounded wait for a barrier's phase: one probe, then suspended waits of 200 us
+// (under a shorter limit, probes) until the phase completes, another role aborts
+// or the limit is over (recorded in *status, first error wins; then *abort is raised).
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                                       uint64_t limit) {
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (limit < 200000u ? mbar_test(bar, parity) : mbar_try_wait_hint(bar, parity, 200000u)) return true;
+    if (*abort) return false;
+    if (globaltimer() - t0 >= limit) {
+      *abort = 1;
+      atomicCAS(status, 0, DT_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool thread_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                                            uint64_t limit) {
+  return mbar_test(bar, parity) || wait_slow(bar, parity, abort, status, limit);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
                                           uint64_t limit) {
-  const bool ok = mbar_wait(bar, parity, abort, status, DT_ERR_TIMEOUT, limit);
-  return __all_sync(0xffffffffu, ok);
+  return __all_sync(0xffffffffu, thread_wait(bar, parity, abort, status, limit));
 }
 
 template <bool F16>
@@ -139,7 +158,7 @@ __device__ __forceinline__ int load_count(const SparseParams& p, int item) {
 }
 __device__ __forceinline__ Item make_item(const SparseParams& p, int item, int rank, int count) {
   Item it;
-  it.h = item / p.nqb;
+  it.h = (int)((unsigned)item / (unsigned)p.nqb);
   it.q0 = (item - it.h * p.nqb) * kTile;
   it.rows = imin(kTile, p.Sq - it.q0);
   it.n = imin(imax(count, 0), p.cap);
@@ -173,6 +192,40 @@ __device__ __forceinline__ Halves tile_halves(const SparseParams& p, const Item&
     v.r1 = 2 * t + 1 >= it.n ? -1 : ((unsigned)e.b < (unsigned)p.nkb ? e.b * 64 : p.Sk);
   }
   return v;
+}
+
+// First tile of an item that holds anything but whole blocks (a short or bad
+// block, or half a tile), by all lanes of a warp: tiles before it need no mask and
+// the softmax warps do not look at their entries.  `ahead`: entries lane,
+// lane + 32, ... of the list, loaded an item earlier.
+constexpr int kAhead = 4;
+__device__ __forceinline__ void load_scan(const SparseParams& p, int item, int lane, int (&ahead)[kAhead]) {
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    ahead[k] = 0;
+    if (item < p.H * p.nqb && lane + 32 * k < p.cap) ahead[k] = ld_ahead(p.idx + (int64_t)item * p.cap + lane + 32 * k);
+  }
+}
+__device__ __forceinline__ int first_masked(const SparseParams& p, const Item& it, int item, int lane,
+                                            const int (&ahead)[kAhead]) {
+  const unsigned whole = (unsigned)p.Sk / (unsigned)(kTile / p.per_tile);     // blocks below this one are whole
+  int at = p.per_tile == 2 && (it.n & 1) ? it.n - 1 : it.n;
+  for (int j = 0; 32 * j < it.n; ++j) {
+    int e = 0;
+    if (j < kAhead) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (k == j) e = ahead[k];
+    } else if (lane + 32 * j < it.n) {
+      e = __ldg(p.idx + (int64_t)item * p.cap + lane + 32 * j);
+    }
+    const uint32_t odd = __ballot_sync(0xffffffffu, lane + 32 * j < it.n && (unsigned)e >= whole);
+    if (odd) {
+      at = imin(at, 32 * j + __ffs(odd) - 1);
+      break;
+    }
+  }
+  return at / p.per_tile;
 }
 
 // Partial O of a split item in shared memory: row-major [128][DP] fp32, 16-byte
@@ -308,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
           if (is_k) {
             const uint32_t b = nq % C::kNQ;
             if (nq >= (uint32_t)C::kNQ &&
-                !mbar_wait(&bars[C::bQEmpty + b], (nq / C::kNQ - 1) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim))
+                !thread_wait(&bars[C::bQEmpty + b], (nq / C::kNQ - 1) & 1, abort_flag, p.status, lim))
               goto tma_done;
             uint8_t* dst = sQ + b * C::kTileBytes;
             mbar_arrive_expect_tx(&bars[C::bQFull + b], C::kTileBytes);
@@ -322,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
             if (t + 1 < it.t1) nxt = load_entries(p, item, t + 1);
             if (is_k && (v.r0 >= p.Sk || (p.per_tile == 2 && v.r1 >= p.Sk))) atomicCAS(p.status, 0, DT_ERR_INVALID);
             const uint32_t st = g % ns;
-            if (g >= ns && !mbar_wait(&empty[st], ((g / ns) - 1) & 1, abort_flag, p.status, DT_ERR_TIMEOUT, lim))
+            if (g >= ns && !thread_wait(&empty[st], ((g / ns) - 1) & 1, abort_flag, p.status, lim))
               goto tma_done;
             uint8_t* dst = ring + st * C::kTileBytes;
             mbar_arrive_expect_tx(&full[st], v.r1 < 0 ? C::kTileBytes / 2 : C::kTileBytes);
@@ -336,13 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         for (uint32_t s = 0; s < ns; ++s)
           if (s < g) {
             const uint32_t last = g - 1 - ((g - 1 - s) % ns);             // latest tile that used stage s
-            mbar_wait(&full[s], (last / ns) & 1, &never, p.status, DT_ERR_TIMEOUT, kDrainLimitNs);
+            thread_wait(&full[s], (last / ns) & 1, &never, p.status, kDrainLimitNs);
           }
         if (is_k)
           for (uint32_t b = 0; b < (uint32_t)C::kNQ; ++b)
             if (b < nq) {
               const uint32_t last = nq - 1 - ((nq - 1 - b) % C::kNQ);
-              mbar_wait(&bars[C::bQFull + b], (last / C::kNQ) & 1, &never, p.status, DT_ERR_TIMEOUT, kDrainLimitNs);
+              thread_wait(&bars[C::bQFull + b], (last / C::kNQ) & 1, &never, p.status, kDrainLimitNs);
             }
       }
       __syncwarp();
@@ -397,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       if (elect_one()) {
         mma_commit(&bars[C::bDrain]);
         volatile int never = 0;
-        mbar_wait(&bars[C::bDrain], 0, &never, p.status, DT_ERR_TIMEOUT, kDrainLimitNs);
+        thread_wait(&bars[C::bDrain], 0, &never, p.status, kDrainLimitNs);
       }
       __syncwarp();
     } else if (warp == kWarpMmaPV) {
@@ -447,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       if (elect_one()) {
         mma_commit(&bars[C::bDrainPV]);
         volatile int never = 0;
-        mbar_wait(&bars[C::bDrainPV], 0, &never, p.status, DT_ERR_TIMEOUT, kDrainLimitNs);
+        thread_wait(&bars[C::bDrainPV], 0, &never, p.status, kDrainLimitNs);
       }
       __syncwarp();
     }
@@ -466,27 +519,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     uint64_t* tok_in = &bars[C::bTok + 2 * pair + (set ^ 1)];
     uint64_t* tok_out = &bars[C::bTok + 2 * pair + set];
     uint32_t g0 = 0, nq = 0;                       // first tile of the item, items done
-    int count = load_count(p, item0);
-    Entries first;
-    {
-      const Item it = make_item(p, item0, rank, count);
-      first = load_entries(p, item0, it.t0 + set);
-    }
+    int count = load_count(p, item0), ahead[kAhead];
+    load_scan(p, item0, lane, ahead);
     for (int item = item0; item < items; item += istep) {
       const Item it = make_item(p, item, rank, count);
       const int nt = it.t1 - it.t0;
-      const int i0 = (g0 & 1) == (uint32_t)set ? 0 : 1;                  // this set's first tile of the item
-      Entries nxt = first;
+      const int masked = first_masked(p, it, item, lane, ahead) - it.t0;   // tiles from this one on may need a mask
       count = load_count(p, item + istep);
-      first = load_entries(p, item + istep, ((g0 + nt) & 1) == (uint32_t)set ? 0 : 1);
+      load_scan(p, item + istep, lane, ahead);
       if (nt == 0) continue;
       const bool idle = pair * 32 >= it.rows;      // none of this warp's rows exist: hand the tiles on
       float m = neg_inf();                          // reference (log2 units) that l stands on
       uint64_t l2[4] = {0ull, 0ull, 0ull, 0ull};    // packed pairs of partial row sums
-      for (int i = i0; i < nt; i += 2) {
+      for (int i = (g0 ^ set) & 1; i < nt; i += 2) {
         const uint32_t g = g0 + i, sb = g % C::kNS;
-        const Halves hv = tile_halves(p, it, it.t0 + i, nxt);
-        if (i + 2 < nt) nxt = load_entries(p, item, it.t0 + i + 2);
         if (!warp_wait(&bars[C::bSFull + sb], (g / C::kNS) & 1, abort_flag, p.status, lim)) goto sm_done;
         if (idle) {
           if (g > 0 && !warp_wait(tok_in, ((g - 1) >> 1) & 1, abort_flag, p.status, lim)) goto sm_done;
@@ -499,9 +545,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         uint32_t sr[128];
 #pragma unroll
         for (int c = 0; c < 128; c += 32) tmem_ld32(sc + c, sr + c);
+        // the reference after the previous tile: usually long there, so it is waited for under the loads
+        if (g > 0 && !warp_wait(tok_in, ((g - 1) >> 1) & 1, abort_flag, p.status, lim)) goto sm_done;
+        const float old = i == 0 ? neg_inf() : s_ref[r];
         tmem_wait_ld();
-        const int v0 = p.Sk - hv.r0, v1 = hv.r1 < 0 ? 0 : p.Sk - hv.r1;      // keys of each half
-        if (v0 < 64 || v1 < 64) {
+        if (i >= masked) {
+          const Halves hv = tile_halves(p, it, it.t0 + i, load_entries(p, item, it.t0 + i));
+          const int v0 = p.Sk - hv.r0, v1 = hv.r1 < 0 ? 0 : p.Sk - hv.r1;    // keys of each half
           // assigned, not added: the logits there may be anything
 #pragma unroll
           for (int e = 0; e < 128; ++e)
@@ -519,9 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         x0 = max3f(x0, u2f(sr[124]), u2f(sr[125]));
         x1 = max3f(x1, u2f(sr[126]), u2f(sr[127]));
         const float mx2 = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * sl2;
-        // the reference after the previous tile, and after this one
-        if (g > 0 && !warp_wait(tok_in, ((g - 1) >> 1) & 1, abort_flag, p.status, lim)) goto sm_done;
-        const float old = i == 0 ? neg_inf() : s_ref[r];
         const float ref = i == 0 ? mx2 : (mx2 > old + kRescaleThreshold ? mx2 : old);
         // a row that has seen only masked keys (reference -inf) has O = 0: it takes the new one without a rescale
         const bool res = ref != old && old != neg_inf();
