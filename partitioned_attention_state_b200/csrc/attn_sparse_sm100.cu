@@ -11,11 +11,15 @@
 // -infinity; the second half of an odd list's last tile is left out of P V
 // altogether, since shared memory there holds earlier keys.
 //
-// A work item is (head, query block).  With at least as many items as SMs the
-// grid is persistent, one CTA per SM striding over the items head-major, so the
-// CTAs that run together read one head's K and V through L2.  With fewer, the
-// `split` CTAs of a cluster take an equal run of the list's tiles each and join
-// their states (m, l, unnormalised O) through distributed shared memory.
+// A work item is (head, query block), and the grid has a CTA per item.  With at
+// least as many items as SMs, a running CTA takes further items over from CTAs
+// that have not started (cluster launch control), an item ahead of its need: the
+// lists may have any lengths, and this balances them without a counter in
+// memory, keeps the items head-major, so that CTAs that run together read one
+// head's K and V through L2, and overlaps one item's end with the next one's
+// start.  With fewer, the `split` CTAs of a cluster take an equal run of the
+// list's tiles each and join their states (m, l, unnormalised O) through
+// distributed shared memory.
 //
 // Per CTA, 16 warps (4 warpgroups, registers rebalanced with setmaxnreg):
 //   warps 0-7   softmax: two sets of four warps that take alternate tiles, a row
@@ -28,8 +32,9 @@
 //   warps 8-11  epilogue: O (TMEM) -> registers, TMEM released, normalised rows
 //               and LSEs to memory, under the next item's tiles
 //   warp 12     tcgen05.mma S = Q K^T; TMEM alloc/free
-//   warp 13     TMA: Q (two buffers) and the K ring
-//   warp 14     TMA: the V ring
+//   warp 13     TMA: Q (two buffers), the K ring and the V ring
+//   warp 14     scheduler: the next item, its list's length, and which of its
+//               tiles need a mask, published to the other roles in shared memory
 //   warp 15     tcgen05.mma O += P V (a second issuing thread: one thread
 //               issues an MMA only every ~50 clk)
 // Tensor memory: three S/P buffers [0,384), O [384,384+DP).
@@ -58,7 +63,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kThreads = 512;
-constexpr int kWarpEpi = 8, kWarpMma = 12, kWarpTmaK = 13, kWarpTmaV = 14, kWarpMmaPV = 15;
+constexpr int kWarpEpi = 8, kWarpMma = 12, kWarpTma = 13, kWarpSched = 14, kWarpMmaPV = 15;
 // Registers per thread at launch (the build checks that ptxas chose them) and
 // the per-warpgroup split, which must fit the launch pool.
 constexpr int kLaunchRegs = 128;
@@ -92,11 +97,12 @@ struct Cfg {
   static constexpr int bQFull = 0, bQEmpty = bQFull + kNQ, bKFull = bQEmpty + kNQ, bVFull = bKFull + kNK,
                        bKEmpty = bVFull + kNV, bVEmpty = bKEmpty + kNK, bSFull = bVEmpty + kNV,
                        bPFull = bSFull + kNS, bPVDone = bPFull + kNS, bOFull = bPVDone + kNS, bOFree = bOFull + 1,
-                       bStFull = bOFree + 1, bStFree = bStFull + 1, bTok = bStFree + 1, bDrain = bTok + 8,
-                       bDrainPV = bDrain + 1, kNumBars = bDrainPV + 1;
+                       bStFull = bOFree + 1, bStFree = bStFull + 1, bTok = bStFree + 1, bInfoFull = bTok + 8,
+                       bInfoFree = bInfoFull + 2, bClc = bInfoFree + 2, bDrain = bClc + 1, bDrainPV = bDrain + 1,
+                       kNumBars = bDrainPV + 1 + (bDrainPV & 1 ? 0 : 1);      // even: what follows is 16-byte aligned
   // per row: reference maximum, and each set's (maximum, sum) of the item
   static constexpr int kStatsBytes = 5 * 128 * 4;
-  static constexpr int kSmem = kTileBytes * (kNQ + kNK + kNV) + kStatsBytes + kNumBars * 8 + 16;
+  static constexpr int kSmem = kTileBytes * (kNQ + kNK + kNV) + kStatsBytes + kNumBars * 8 + 2 * 48 + 16 + 16;
   static_assert(kSmem <= 232448, "shared memory budget");
   // a split item's partial O ([128][DP] fp32) reuses the K ring, drained by then
   static_assert(kNK * kTileBytes >= 128 * DP * 4, "partial O fits the K ring");
@@ -142,41 +148,28 @@ __host__ __device__ constexpr uint32_t idesc16(int M, int N, int b_mn) {
   return F16 ? d & ~((1u << 7) | (1u << 10)) : d;
 }
 
-// One item's list: entries [0, n), of which this CTA takes tiles [t0, t1).
-// The list's length and its first entries are loaded an item ahead, and every
-// other entry a tile ahead: a load from L2 costs as much as a third of a tile,
-// and two one after another at every item cost each role 1-2 us.
-// Volatile, or the compiler moves the load down to the value's use.
+// One item, as the scheduler publishes it: entries [0, n) of list `item`, of
+// which this CTA takes tiles [t0, t0 + nt); h < 0 ends the sequence.  Tiles from
+// `masked` on may hold less than whole blocks (a short or bad one, or half a
+// tile): the softmax looks at the entries of those alone.  first_a, first_b:
+// the entries of tile t0.
+struct __align__(16) Item { int h, q0, rows, item, n, t0, nt, masked, first_a, first_b, pad0, pad1; };
+static_assert(sizeof(Item) == 48, "Item in shared memory");
+
+// The entries of tile t of a list (b: -1 past its end).  Volatile, or the
+// compiler moves a load that was issued a tile ahead down to the value's use.
 __device__ __forceinline__ int ld_ahead(const int32_t* a) {
   int v;
   asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(a));
   return v;
 }
-struct Item { int h, q0, rows, n, t0, t1; };
-__device__ __forceinline__ int load_count(const SparseParams& p, int item) {
-  return p.count && item < p.H * p.nqb ? ld_ahead(p.count + item) : p.cap;
-}
-__device__ __forceinline__ Item make_item(const SparseParams& p, int item, int rank, int count) {
-  Item it;
-  it.h = (int)((unsigned)item / (unsigned)p.nqb);
-  it.q0 = (item - it.h * p.nqb) * kTile;
-  it.rows = imin(kTile, p.Sq - it.q0);
-  it.n = imin(imax(count, 0), p.cap);
-  const int nt = (it.n + p.per_tile - 1) / p.per_tile;
-  it.t0 = p.split == 1 ? 0 : (int)((int64_t)nt * rank / p.split);
-  it.t1 = p.split == 1 ? nt : (int)((int64_t)nt * (rank + 1) / p.split);
-  return it;
-}
-// The entries of tile t of an item's list, as loaded (none past the list's allocation).
 struct Entries { int a, b; };
-__device__ __forceinline__ Entries load_entries(const SparseParams& p, int item, int t) {
+__device__ __forceinline__ Entries load_entries(const SparseParams& p, const Item& it, int t) {
   Entries e = {-1, -1};
   const int i = t * p.per_tile;
-  if (item < p.H * p.nqb && i < p.cap) {
-    const int32_t* l = p.idx + (int64_t)item * p.cap + i;
-    e.a = ld_ahead(l);
-    if (p.per_tile == 2 && i + 1 < p.cap) e.b = ld_ahead(l + 1);
-  }
+  const int32_t* l = p.idx + (int64_t)it.item * p.cap + i;
+  if (i < it.n) e.a = ld_ahead(l);
+  if (p.per_tile == 2 && i + 1 < it.n) e.b = ld_ahead(l + 1);
   return e;
 }
 // First key rows of the two 64-row halves of tile t; Sk (nothing there) for an
@@ -193,39 +186,66 @@ __device__ __forceinline__ Halves tile_halves(const SparseParams& p, const Item&
   }
   return v;
 }
-
-// First tile of an item that holds anything but whole blocks (a short or bad
-// block, or half a tile), by all lanes of a warp: tiles before it need no mask and
-// the softmax warps do not look at their entries.  `ahead`: entries lane,
-// lane + 32, ... of the list, loaded an item earlier.
-constexpr int kAhead = 4;
-__device__ __forceinline__ void load_scan(const SparseParams& p, int item, int lane, int (&ahead)[kAhead]) {
-#pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    ahead[k] = 0;
-    if (item < p.H * p.nqb && lane + 32 * k < p.cap) ahead[k] = ld_ahead(p.idx + (int64_t)item * p.cap + lane + 32 * k);
-  }
-}
-__device__ __forceinline__ int first_masked(const SparseParams& p, const Item& it, int item, int lane,
-                                            const int (&ahead)[kAhead]) {
+// Item `item` (>= 0) for rank `rank` of its cluster, by all lanes of a warp:
+// reads the whole list once, reports what is wrong with it.
+__device__ __forceinline__ Item make_item(const SparseParams& p, int item, int rank, int lane) {
+  Item it = {};
+  it.item = item;
+  it.h = (int)((unsigned)item / (unsigned)p.nqb);
+  it.q0 = (item - it.h * p.nqb) * kTile;
+  it.rows = imin(kTile, p.Sq - it.q0);
+  const int count = p.count ? __ldg(p.count + item) : p.cap;
+  it.n = imin(imax(count, 0), p.cap);
+  const int nt = (it.n + p.per_tile - 1) / p.per_tile;
+  it.t0 = (int)((int64_t)nt * rank / p.split);
+  it.nt = (int)((int64_t)nt * (rank + 1) / p.split) - it.t0;
   const unsigned whole = (unsigned)p.Sk / (unsigned)(kTile / p.per_tile);     // blocks below this one are whole
+  const int32_t* list = p.idx + (int64_t)item * p.cap;
   int at = p.per_tile == 2 && (it.n & 1) ? it.n - 1 : it.n;
-  for (int j = 0; 32 * j < it.n; ++j) {
-    int e = 0;
-    if (j < kAhead) {
+  bool bad = count != it.n;
+  for (int j = 0; j < it.n; j += 128) {
+    int e[4];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (k == j) e = ahead[k];
-    } else if (lane + 32 * j < it.n) {
-      e = __ldg(p.idx + (int64_t)item * p.cap + lane + 32 * j);
-    }
-    const uint32_t odd = __ballot_sync(0xffffffffu, lane + 32 * j < it.n && (unsigned)e >= whole);
-    if (odd) {
-      at = imin(at, 32 * j + __ffs(odd) - 1);
-      break;
+    for (int k = 0; k < 4; ++k) e[k] = j + 32 * k + lane < it.n ? __ldg(list + j + 32 * k + lane) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool in = j + 32 * k + lane < it.n;
+      const uint32_t odd = __ballot_sync(0xffffffffu, in && (unsigned)e[k] >= whole);
+      if (odd) at = imin(at, j + 32 * k + __ffs(odd) - 1);
+      bad |= in && (unsigned)e[k] >= (unsigned)p.nkb;
     }
   }
-  return at / p.per_tile;
+  it.masked = at / p.per_tile;
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && rank == 0) atomicCAS(p.status, 0, DT_ERR_INVALID);
+  const Entries f = load_entries(p, it, it.t0);
+  it.first_a = f.a;
+  it.first_b = f.b;
+  return it;
+}
+
+// Cluster launch control: ask for a CTA of the grid that has not started, to be
+// run here instead; the 16-byte answer lands in shared memory and completes on
+// `bar`.  Returns its index, or -1 where none was left.
+__device__ __forceinline__ void clc_ask(uint32_t answer, uint64_t* bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ int clc_answer(uint32_t answer) {
+  uint32_t ok, x = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t"
+      "ld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return ok ? (int)x : -1;
 }
 
 // Partial O of a split item in shared memory: row-major [128][DP] fp32, 16-byte
@@ -292,16 +312,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
   float* stat_l = stat_m + 256;                                              // [2 sets][128]
   float* s_ref = stat_l + 256;                                               // [128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_ref + 128);
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+  Item* info = reinterpret_cast<Item*>(bars + C::kNumBars);                  // [2]
+  uint32_t* clc = reinterpret_cast<uint32_t*>(info + 2);                     // [4]
+  uint32_t* tmem_holder = clc + 4;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t lim = p.wait_limit_ns;
   const int rank = p.split > 1 ? (int)cluster_rank() : 0;
-  const int items = p.H * p.nqb;
-  const int item0 = blockIdx.x / p.split, istep = gridDim.x / p.split;
 
-  if (warp == kWarpTmaK && lane == 0) {
+  if (warp == kWarpTma && lane == 0) {
     for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bars[i], 1);
     // every thread of the arriving role arrives (no single-lane branches)
     for (int i = 0; i < C::kNS; ++i) mbar_init(&bars[C::bPFull + i], 4 * 32);
@@ -309,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     mbar_init(&bars[C::bStFull], 8 * 32);
     mbar_init(&bars[C::bStFree], 4 * 32);
     mbar_init(&bars[C::bOFree], 4 * 32);
+    // readers of an item: TMA thread, two MMA warps, softmax, epilogue
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[C::bInfoFree + i], 1 + 2 * 32 + 8 * 32 + 4 * 32);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async();
@@ -321,25 +343,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  // The seq-th item for this role (warp-wide); false at the end or after an abort.
+  auto next_item = [&](uint32_t seq, Item& it) {
+    if (!warp_wait(&bars[C::bInfoFull + (seq & 1)], (seq >> 1) & 1, abort_flag, p.status, lim)) return false;
+    it = info[seq & 1];
+    mbar_arrive(&bars[C::bInfoFree + (seq & 1)]);
+    return it.h >= 0;
+  };
 
   if (warp >= kWarpMma) {
     regs_set<kLaunchRegs, kRegsOther>();
-    if (warp == kWarpTmaK || warp == kWarpTmaV) {
-      // ---------------------------------------------------------- TMA producers
+    if (warp == kWarpSched) {
+      // ---------------------------------------------------------- scheduler
+      const uint32_t answer = smem_u32(clc);
+      int item = blockIdx.x / p.split;
+      for (uint32_t seq = 0;; ++seq) {
+        const bool ask = item >= 0 && p.split == 1;       // the item after this one
+        if (ask && lane == 0) clc_ask(answer, &bars[C::bClc]);
+        Item it = {};
+        it.h = -1;
+        if (item >= 0) it = make_item(p, item, rank, lane);
+        bool ok = seq < 2 || warp_wait(&bars[C::bInfoFree + (seq & 1)], ((seq >> 1) - 1) & 1, abort_flag, p.status, lim);
+        if (ok) {
+          if (lane == 0) {
+            info[seq & 1] = it;
+            mbar_arrive(&bars[C::bInfoFull + (seq & 1)]);
+          }
+          __syncwarp();
+        }
+        if (ask) {                                        // waited for after an abort too: the answer is in flight
+          volatile int never = 0;
+          ok = __all_sync(0xffffffffu, thread_wait(&bars[C::bClc], seq & 1, &never, p.status, kDrainLimitNs)) && ok;
+        }
+        if (!ok || it.h < 0) break;
+        item = ask ? clc_answer(answer) : -1;
+        fence_proxy_async();                              // the answer is read before the next one overwrites it
+        __syncwarp();
+      }
+    } else if (warp == kWarpTma) {
+      // ---------------------------------------------------------- TMA producer
       if (lane == 0) {
-        const bool is_k = warp == kWarpTmaK;
-        const CUtensorMap* tm = is_k ? &p.tmK : &p.tmV;
-        const CUtensorMap* tmt = is_k ? &p.tmKt : &p.tmVt;
-        uint8_t* ring = is_k ? sK : sV;
-        const uint32_t ns = is_k ? C::kNK : C::kNV;
-        uint64_t* full = &bars[is_k ? C::bKFull : C::bVFull];
-        uint64_t* empty = &bars[is_k ? C::bKEmpty : C::bVEmpty];
-        prefetch_tmap(tm);
-        if (C::kTail) prefetch_tmap(tmt);
-        if (is_k) { prefetch_tmap(&p.tmQ); if (C::kTail) prefetch_tmap(&p.tmQt); }
+        prefetch_tmap(&p.tmQ);
+        prefetch_tmap(&p.tmK);
+        prefetch_tmap(&p.tmV);
+        if (C::kTail) {
+          prefetch_tmap(&p.tmQt);
+          prefetch_tmap(&p.tmKt);
+          prefetch_tmap(&p.tmVt);
+        }
         // K/V blocks are read by many query blocks of the head; a Q tile once
         const uint64_t pol_keep = l2_policy_evict_last(), pol_once = l2_policy_evict_first();
-        uint32_t g = 0, nq = 0;
+        uint32_t gk = 0, gv = 0, nq = 0;                  // K tiles, V tiles, Q tiles issued
         // 64 rows from row0 of a K, V or Q head, into half `half` of a tile
         auto load_half = [&](const CUtensorMap* t64, const CUtensorMap* t16, uint8_t* tile, uint64_t* bar, int half,
                              int row0, int h, uint64_t pol) {
@@ -349,54 +403,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
           if (C::kTail)
             tma_load_3d_hint(tile + C::kN64 * C::kBlk + half * (C::kTailBytes / 2), t16, bar, 64 * C::kN64, row0, h, pol);
         };
-        int count = load_count(p, item0);
-        Entries first = load_entries(p, item0, make_item(p, item0, rank, count).t0);
-        for (int item = item0; item < items; item += istep) {
-          const Item it = make_item(p, item, rank, count);
-          if (is_k && rank == 0 && count != it.n) atomicCAS(p.status, 0, DT_ERR_INVALID);
-          Entries nxt = first;
-          count = load_count(p, item + istep);
-          first = load_entries(p, item + istep, 0);
-          if (it.t0 == it.t1) continue;
-          if (is_k) {
-            const uint32_t b = nq % C::kNQ;
-            if (nq >= (uint32_t)C::kNQ &&
-                !thread_wait(&bars[C::bQEmpty + b], (nq / C::kNQ - 1) & 1, abort_flag, p.status, lim))
-              goto tma_done;
-            uint8_t* dst = sQ + b * C::kTileBytes;
-            mbar_arrive_expect_tx(&bars[C::bQFull + b], C::kTileBytes);
-            load_half(&p.tmQ, &p.tmQt, dst, &bars[C::bQFull + b], 0, it.q0, it.h, pol_once);
-            load_half(&p.tmQ, &p.tmQt, dst, &bars[C::bQFull + b], 1, it.q0 + 64, it.h, pol_once);
-            ++nq;
-          }
+        Halves vp = {0, 0};                               // the tile whose V is still to be issued
+        int vh = -1;
+        auto issue_v = [&]() {
+          if (vh < 0) return true;
+          const uint32_t st = gv % C::kNV;
+          if (gv >= (uint32_t)C::kNV &&
+              !thread_wait(&bars[C::bVEmpty + st], ((gv / C::kNV) - 1) & 1, abort_flag, p.status, lim))
+            return false;
+          uint8_t* dst = sV + st * C::kTileBytes;
+          uint64_t* full = &bars[C::bVFull + st];
+          mbar_arrive_expect_tx(full, vp.r1 < 0 ? C::kTileBytes / 2 : C::kTileBytes);
+          load_half(&p.tmV, &p.tmVt, dst, full, 0, vp.r0, vh, pol_keep);
+          if (vp.r1 >= 0) load_half(&p.tmV, &p.tmVt, dst, full, 1, vp.r1, vh, pol_keep);
+          vh = -1;
+          ++gv;
+          return true;
+        };
+        // V(g) goes out after K(g+1): the order in which their stages fall free
+        for (uint32_t seq = 0;; ++seq) {
+          uint64_t* ready = &bars[C::bInfoFull + (seq & 1)];
+          if (!mbar_test(ready, (seq >> 1) & 1) &&
+              (!issue_v() || !thread_wait(ready, (seq >> 1) & 1, abort_flag, p.status, lim)))
+            break;
+          const Item it = info[seq & 1];
+          mbar_arrive(&bars[C::bInfoFree + (seq & 1)]);
+          if (it.h < 0) break;
+          if (it.nt == 0) continue;
+          const uint32_t b = nq % C::kNQ;
+          if (nq >= (uint32_t)C::kNQ &&
+              !thread_wait(&bars[C::bQEmpty + b], (nq / C::kNQ - 1) & 1, abort_flag, p.status, lim))
+            goto tma_done;
+          mbar_arrive_expect_tx(&bars[C::bQFull + b], C::kTileBytes);
+          load_half(&p.tmQ, &p.tmQt, sQ + b * C::kTileBytes, &bars[C::bQFull + b], 0, it.q0, it.h, pol_once);
+          load_half(&p.tmQ, &p.tmQt, sQ + b * C::kTileBytes, &bars[C::bQFull + b], 1, it.q0 + 64, it.h, pol_once);
+          ++nq;
           const int hk = it.h / p.per_kv;
-          for (int t = it.t0; t < it.t1; ++t, ++g) {
+          Entries nxt = {it.first_a, it.first_b};
+          for (int t = it.t0; t < it.t0 + it.nt; ++t) {
             const Halves v = tile_halves(p, it, t, nxt);
-            if (t + 1 < it.t1) nxt = load_entries(p, item, t + 1);
-            if (is_k && (v.r0 >= p.Sk || (p.per_tile == 2 && v.r1 >= p.Sk))) atomicCAS(p.status, 0, DT_ERR_INVALID);
-            const uint32_t st = g % ns;
-            if (g >= ns && !thread_wait(&empty[st], ((g / ns) - 1) & 1, abort_flag, p.status, lim))
+            if (t + 1 < it.t0 + it.nt) nxt = load_entries(p, it, t + 1);
+            const uint32_t st = gk % C::kNK;
+            if (gk >= (uint32_t)C::kNK &&
+                !thread_wait(&bars[C::bKEmpty + st], ((gk / C::kNK) - 1) & 1, abort_flag, p.status, lim))
               goto tma_done;
-            uint8_t* dst = ring + st * C::kTileBytes;
-            mbar_arrive_expect_tx(&full[st], v.r1 < 0 ? C::kTileBytes / 2 : C::kTileBytes);
-            load_half(tm, tmt, dst, &full[st], 0, v.r0, hk, pol_keep);
-            if (v.r1 >= 0) load_half(tm, tmt, dst, &full[st], 1, v.r1, hk, pol_keep);
+            uint8_t* dst = sK + st * C::kTileBytes;
+            uint64_t* full = &bars[C::bKFull + st];
+            mbar_arrive_expect_tx(full, v.r1 < 0 ? C::kTileBytes / 2 : C::kTileBytes);
+            load_half(&p.tmK, &p.tmKt, dst, full, 0, v.r0, hk, pol_keep);
+            if (v.r1 >= 0) load_half(&p.tmK, &p.tmKt, dst, full, 1, v.r1, hk, pol_keep);
+            ++gk;
+            if (!issue_v()) goto tma_done;
+            vp = v;
+            vh = hk;
           }
         }
+        issue_v();
       tma_done:
-        // let every copy this warp started land before shared memory goes away
+        // let every copy this thread started land before shared memory goes away
         volatile int never = 0;
-        for (uint32_t s = 0; s < ns; ++s)
-          if (s < g) {
-            const uint32_t last = g - 1 - ((g - 1 - s) % ns);             // latest tile that used stage s
-            thread_wait(&full[s], (last / ns) & 1, &never, p.status, kDrainLimitNs);
-          }
-        if (is_k)
-          for (uint32_t b = 0; b < (uint32_t)C::kNQ; ++b)
-            if (b < nq) {
-              const uint32_t last = nq - 1 - ((nq - 1 - b) % C::kNQ);
-              thread_wait(&bars[C::bQFull + b], (last / C::kNQ) & 1, &never, p.status, kDrainLimitNs);
-            }
+        auto drain = [&](int bar, uint32_t stages, uint32_t n) {
+          for (uint32_t s = 0; s < stages; ++s)
+            if (s < n)                                    // the latest tile that used stage s
+              thread_wait(&bars[bar + s], ((n - 1 - ((n - 1 - s) % stages)) / stages) & 1, &never, p.status, kDrainLimitNs);
+        };
+        drain(C::bKFull, C::kNK, gk);
+        drain(C::bVFull, C::kNV, gv);
+        drain(C::bQFull, C::kNQ, nq);
       }
       __syncwarp();
     } else if (warp == kWarpMma) {
@@ -412,15 +485,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       const uint64_t kt0 = smem_desc(smem_u32(sK) + C::kN64 * C::kBlk, 16, 256, kSwizzle32B);
       uint32_t g = 0, nq = 0;
       bool ok = true;
-      int count = load_count(p, item0);
-      for (int item = item0; item < items && ok; item += istep) {
-        const Item it = make_item(p, item, rank, count);
-        count = load_count(p, item + istep);
-        if (it.t0 == it.t1) continue;
+      Item it;
+      for (uint32_t seq = 0; ok && next_item(seq, it); ++seq) {
+        if (it.nt == 0) continue;
         const uint32_t qb = nq % C::kNQ;
         ok = warp_wait(&bars[C::bQFull + qb], (nq / C::kNQ) & 1, abort_flag, p.status, lim);
         ++nq;
-        for (int t = it.t0; t < it.t1 && ok; ++t, ++g) {
+        for (int t = 0; t < it.nt && ok; ++t, ++g) {
           const uint32_t st = g % C::kNK, sb = g % C::kNS;
           // K has arrived, and S buffer sb, which held P(g-3), is free: its P V (issued by warp 15) is done
           ok = warp_wait(&bars[C::bKFull + st], (g / C::kNK) & 1, abort_flag, p.status, lim) &&
@@ -441,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
               mma_ss(dS, qt0 + qb * (C::kTileBytes >> 4), kt0 + st * (C::kTileBytes >> 4), idesc, 1u);
             mma_commit(&bars[C::bSFull + sb]);
             mma_commit(&bars[C::bKEmpty + st]);
-            if (t == it.t1 - 1) mma_commit(&bars[C::bQEmpty + qb]);
+            if (t == it.nt - 1) mma_commit(&bars[C::bQEmpty + qb]);
           }
           __syncwarp();
         }
@@ -461,22 +532,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       const uint64_t vt0 = smem_desc(smem_u32(sV) + C::kN64 * C::kBlk, C::kTailBytes, 256, kSwizzle32B);
       uint32_t g = 0, nq = 0;
       bool ok = true;
-      int count = load_count(p, item0);
-      for (int item = item0; item < items && ok; item += istep) {
-        const Item it = make_item(p, item, rank, count);
-        count = load_count(p, item + istep);
-        if (it.t0 == it.t1) continue;
-        for (int t = it.t0; t < it.t1 && ok; ++t, ++g) {
+      Item it;
+      for (uint32_t seq = 0; ok && next_item(seq, it); ++seq) {
+        if (it.nt == 0) continue;
+        for (int t = 0; t < it.nt && ok; ++t, ++g) {
           const uint32_t sb = g % C::kNS, st = g % C::kNV;
           ok = warp_wait(&bars[C::bVFull + st], (g / C::kNV) & 1, abort_flag, p.status, lim) &&
-               (t > it.t0 || nq == 0 || warp_wait(&bars[C::bOFree], (nq - 1) & 1, abort_flag, p.status, lim)) &&
+               (t > 0 || nq == 0 || warp_wait(&bars[C::bOFree], (nq - 1) & 1, abort_flag, p.status, lim)) &&
                warp_wait(&bars[C::bPFull + sb], (g / C::kNS) & 1, abort_flag, p.status, lim);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
             const uint32_t aP = tmem + C::kColS + sb * 128;
             const uint64_t vd = vd0 + st * (C::kTileBytes >> 4), vdt = vt0 + st * (C::kTileBytes >> 4);
-            const uint32_t acc = t > it.t0 ? 1u : 0u;
+            const uint32_t acc = t > 0 ? 1u : 0u;
             // 16 keys per MMA: descriptors advance by 16 V rows
             auto pv = [&](int kk) {
               mma_ts(tmem + C::kColO, aP + 8 * kk, vd + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1u : acc);
@@ -485,13 +554,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
             };
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) pv(kk);
-            if (p.per_tile == 1 || 2 * t + 1 < it.n) {      // a tile that holds one 64-key block ends here
+            if (p.per_tile == 1 || 2 * (it.t0 + t) + 1 < it.n) {      // a tile that holds one 64-key block ends here
 #pragma unroll
               for (int kk = 4; kk < 8; ++kk) pv(kk);
             }
             mma_commit(&bars[C::bVEmpty + st]);
             mma_commit(&bars[C::bPVDone + sb]);
-            if (t == it.t1 - 1) mma_commit(&bars[C::bOFull]);
+            if (t == it.nt - 1) mma_commit(&bars[C::bOFull]);
           }
           __syncwarp();
         }
@@ -519,14 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     uint64_t* tok_in = &bars[C::bTok + 2 * pair + (set ^ 1)];
     uint64_t* tok_out = &bars[C::bTok + 2 * pair + set];
     uint32_t g0 = 0, nq = 0;                       // first tile of the item, items done
-    int count = load_count(p, item0), ahead[kAhead];
-    load_scan(p, item0, lane, ahead);
-    for (int item = item0; item < items; item += istep) {
-      const Item it = make_item(p, item, rank, count);
-      const int nt = it.t1 - it.t0;
-      const int masked = first_masked(p, it, item, lane, ahead) - it.t0;   // tiles from this one on may need a mask
-      count = load_count(p, item + istep);
-      load_scan(p, item + istep, lane, ahead);
+    Item it;
+    for (uint32_t seq = 0; next_item(seq, it); ++seq) {
+      const int nt = it.nt, masked = it.masked - it.t0;  // tiles from `masked` on may need a mask
       if (nt == 0) continue;
       const bool idle = pair * 32 >= it.rows;      // none of this warp's rows exist: hand the tiles on
       float m = neg_inf();                          // reference (log2 units) that l stands on
@@ -550,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         const float old = i == 0 ? neg_inf() : s_ref[r];
         tmem_wait_ld();
         if (i >= masked) {
-          const Halves hv = tile_halves(p, it, it.t0 + i, load_entries(p, item, it.t0 + i));
+          const Halves hv = tile_halves(p, it, it.t0 + i, load_entries(p, it, it.t0 + i));
           const int v0 = p.Sk - hv.r0, v1 = hv.r1 < 0 ? 0 : p.Sk - hv.r1;    // keys of each half
           // assigned, not added: the logits there may be anything
 #pragma unroll
@@ -636,14 +700,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     const int r = (warp - kWarpEpi) * 32 + lane;          // tile row of this thread
     const uint32_t oaddr = tmem + (static_cast<uint32_t>((warp - kWarpEpi) * 32) << 16) + C::kColO;
     uint32_t nq = 0;
-    int count = load_count(p, item0);
-    for (int item = item0; item < items; item += istep) {
-      const Item it = make_item(p, item, rank, count);
-      count = load_count(p, item + istep);
+    Item it;
+    for (uint32_t seq = 0; next_item(seq, it); ++seq) {
       const bool valid = r < it.rows;
       const int64_t orow = it.h * p.o_head + (int64_t)(it.q0 + r) * p.o_row;
       float* lrow = p.L + (int64_t)it.h * p.Sq + it.q0 + r;
-      if (it.t0 == it.t1) {
+      if (it.nt == 0) {
         if (p.split > 1) {                                // an empty state for the join
           stat_m[r] = neg_inf();
           stat_l[r] = 0.f;
@@ -710,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     __syncwarp();
     cluster_sync_all();
     if (warp >= kWarpEpi && warp < kWarpMma && !*abort_flag) {
-      const Item it = make_item(p, item0, rank, load_count(p, item0));
+      const Item it = info[0];                            // the one item, untouched since
       const uint32_t a_m = smem_u32(stat_m), a_l = smem_u32(stat_l), a_o = smem_u32(sK);
       const int nchunk = it.rows * (D / 8);
       for (int i = (threadIdx.x - kWarpEpi * 32) * p.split + rank; i < nchunk; i += 128 * p.split) {
@@ -792,7 +854,7 @@ int launch_dp(SparseParams& p, int sms, cudaStream_t stream) {
       if (items <= clusters[dev][s].load(std::memory_order_relaxed)) p.split = s;
   attr.val.clusterDim.x = p.split;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
-  cfg.gridDim = dim3((unsigned)(p.split > 1 ? items * p.split : (items < sms ? items : sms)));
+  cfg.gridDim = dim3((unsigned)(items * p.split));
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? DT_OK : DT_ERR_CUDA;
 }
 
