@@ -332,9 +332,9 @@ bool strides_nonneg(const dt_strides& s, int heads, int rows) {
   return (heads <= 1 || s.head >= 0) && (rows <= 1 || s.row >= 0);
 }
 
-// 16-bit [heads][S][D] with element strides as a 3-D tensor (D, S, heads); box (bw, 64, 1)
+// 16-bit [heads][S][D] with element strides as a 3-D tensor (D, S, heads); box (bw, rows, 1)
 bool encode_strided(CUtensorMap* m, const void* base, int heads, int S, int D, dt_strides st, bool f16, int bw,
-                    CUtensorMapSwizzle sw) {
+                    CUtensorMapSwizzle sw, int rows = 64) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)S, (cuuint64_t)heads};
@@ -342,7 +342,7 @@ bool encode_strided(CUtensorMap* m, const void* base, int heads, int S, int D, d
   const cuuint64_t row = S > 1 ? (cuuint64_t)st.row * 2 : (cuuint64_t)((D * 2 + 15) / 16 * 16);
   const cuuint64_t head = heads > 1 ? (cuuint64_t)st.head * 2 : row;
   cuuint64_t strides[2] = {row, head};
-  cuuint32_t box[3] = {(cuuint32_t)bw, 64u, 1u};
+  cuuint32_t box[3] = {(cuuint32_t)bw, (cuuint32_t)rows, 1u};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -483,6 +483,9 @@ extern "C" int dt_attn_block_sparse(const dt_sparse_params* p, const void* Q, co
     ok = encode_strided(&kp.tmQt, Q, p->H, p->Sq, p->D, p->q, f16, 16, sw32) &&
          encode_strided(&kp.tmKt, Kb, kh, kr, p->D, p->k, f16, 16, sw32) &&
          encode_strided(&kp.tmVt, Vb, kh, kr, p->D, p->v, f16, 16, sw32);
+  if (ok && p->out_type != DT_TYPE_F32)
+    ok = encode_strided(&kp.tmO, O, p->H, p->Sq, p->D, p->o, f16, 64, sw128, 32) &&
+         (p->D != 72 || encode_strided(&kp.tmOt, O, p->H, p->Sq, p->D, p->o, f16, 8, CU_TENSOR_MAP_SWIZZLE_NONE, 32));
   if (!ok) return DT_ERR_CUDA;
   kp.idx = idx;
   kp.count = count;

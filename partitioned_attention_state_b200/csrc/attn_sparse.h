@@ -10,6 +10,7 @@ namespace dt {
 struct SparseParams {
   CUtensorMap tmQ, tmK, tmV;        // 64-column blocks of 64 rows, 128-byte swizzle
   CUtensorMap tmQt, tmKt, tmVt;     // 16-column tail block (D = 72), 32-byte swizzle
+  CUtensorMap tmO, tmOt;            // 16-bit output: boxes of 32 rows, 64 columns (128-byte swizzle) and the 8 of the tail
   const int32_t* idx;               // [H][nqb][cap]
   const int32_t* count;             // [H][nqb] or null (cap each)
   void* O;

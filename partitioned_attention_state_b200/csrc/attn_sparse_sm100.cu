@@ -29,8 +29,11 @@
 //               takes its maxima.  Both scale by one reference maximum per row,
 //               handed from set to set in shared memory, so that O stays a single
 //               accumulator; a row's sum is kept by each set and added at the end
-//   warps 8-11  epilogue: O (TMEM) -> registers, TMEM released, normalised rows
-//               and LSEs to memory, under the next item's tiles
+//   warps 8-11  epilogue, under the next item's tiles: O (TMEM) normalised and
+//               rounded into the item's own Q buffer, whence TMA stores it.  A
+//               row per lane stored straight to memory put 32 sectors in 32
+//               lines into every instruction and held up the SM's load/store
+//               unit, which the softmax needs, for 2,000 clk per item
 //   warp 12     tcgen05.mma S = Q K^T; TMEM alloc/free
 //   warp 13     TMA: Q (two buffers), the K ring and the V ring
 //   warp 14     scheduler: the next item, its list's length, and which of its
@@ -67,7 +70,7 @@ constexpr int kWarpEpi = 8, kWarpMma = 12, kWarpTma = 13, kWarpSched = 14, kWarp
 // Registers per thread at launch (the build checks that ptxas chose them) and
 // the per-warpgroup split, which must fit the launch pool.
 constexpr int kLaunchRegs = 128;
-constexpr int kRegsSoftmax = 184, kRegsEpilogue = 96, kRegsOther = 48;
+constexpr int kRegsSoftmax = 192, kRegsEpilogue = 80, kRegsOther = 48;
 static_assert(128 * (2 * kRegsSoftmax + kRegsEpilogue + kRegsOther) <= kThreads * kLaunchRegs, "register split");
 constexpr uint64_t kDrainLimitNs = 1000000000ull;
 constexpr int kMaxDevices = 64;
@@ -282,6 +285,13 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
   return v;
 }
 
+// Ties values loaded from tensor memory to the wait that precedes this: no use of theirs moves above it.
+template <int N>
+__device__ __forceinline__ void after_wait(uint32_t* r) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
 // 8 columns of an output row
 template <bool F16>
 __device__ __forceinline__ void store_out8(const SparseParams& p, int64_t off, const float* x) {
@@ -328,6 +338,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     for (int i = 0; i < 8; ++i) mbar_init(&bars[C::bTok + i], 32);
     mbar_init(&bars[C::bStFull], 8 * 32);
     mbar_init(&bars[C::bStFree], 4 * 32);
+    // a Q buffer is free when its last Q K^T is done and the 4 epilogue warps have stored O from it
+    for (int i = 0; i < C::kNQ; ++i) mbar_init(&bars[C::bQEmpty + i], 1 + 4);
     mbar_init(&bars[C::bOFree], 4 * 32);
     // readers of an item: TMA thread, two MMA warps, softmax, epilogue
     for (int i = 0; i < 2; ++i) mbar_init(&bars[C::bInfoFree + i], 1 + 2 * 32 + 8 * 32 + 4 * 32);
@@ -607,13 +619,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         tc_fence_after();
         const uint32_t sc = tmem + lane_base + C::kColS + sb * 128;
         uint32_t sr[128];
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld32(sc + c, sr + c);
+        tmem_ld32(sc, sr);
+        tmem_ld32(sc + 32, sr + 32);
         // the reference after the previous tile: usually long there, so it is waited for under the loads
         if (g > 0 && !warp_wait(tok_in, ((g - 1) >> 1) & 1, abort_flag, p.status, lim)) goto sm_done;
         const float old = i == 0 ? neg_inf() : s_ref[r];
         tmem_wait_ld();
-        if (i >= masked) {
+        after_wait<64>(sr);
+        tmem_ld32(sc + 64, sr + 64);
+        tmem_ld32(sc + 96, sr + 96);
+        // maxima in four chains; the first half's under the second half's loads
+        float x[4];
+        auto chain = [&](int e0) {
+#pragma unroll
+          for (int e = e0; e < e0 + 64; e += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = e == 0 ? fmaxf(u2f(sr[2 * k]), u2f(sr[2 * k + 1]))
+                            : max3f(x[k], u2f(sr[e + 2 * k]), u2f(sr[e + 2 * k + 1]));
+        };
+        const bool mask = i >= masked;
+        if (!mask) chain(0);
+        tmem_wait_ld();
+        after_wait<64>(sr + 64);
+        if (mask) {
           const Halves hv = tile_halves(p, it, it.t0 + i, load_entries(p, it, it.t0 + i));
           const int v0 = p.Sk - hv.r0, v1 = hv.r1 < 0 ? 0 : p.Sk - hv.r1;    // keys of each half
           // assigned, not added: the logits there may be anything
@@ -621,18 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
           for (int e = 0; e < 128; ++e)
             if (!((e & 63) < (e < 64 ? v0 : v1))) sr[e] = f2u(neg_inf());
         }
-        float x0 = max3f(u2f(sr[0]), u2f(sr[1]), u2f(sr[2])), x1 = max3f(u2f(sr[3]), u2f(sr[4]), u2f(sr[5]));
-        float x2 = max3f(u2f(sr[6]), u2f(sr[7]), u2f(sr[8])), x3 = max3f(u2f(sr[9]), u2f(sr[10]), u2f(sr[11]));
-#pragma unroll
-        for (int e = 12; e < 124; e += 8) {
-          x0 = max3f(x0, u2f(sr[e]), u2f(sr[e + 1]));
-          x1 = max3f(x1, u2f(sr[e + 2]), u2f(sr[e + 3]));
-          x2 = max3f(x2, u2f(sr[e + 4]), u2f(sr[e + 5]));
-          x3 = max3f(x3, u2f(sr[e + 6]), u2f(sr[e + 7]));
-        }
-        x0 = max3f(x0, u2f(sr[124]), u2f(sr[125]));
-        x1 = max3f(x1, u2f(sr[126]), u2f(sr[127]));
-        const float mx2 = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * sl2;
+        if (mask) chain(0);
+        chain(64);
+        const float mx2 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
         const float ref = i == 0 ? mx2 : (mx2 > old + kRescaleThreshold ? mx2 : old);
         // a row that has seen only masked keys (reference -inf) has O = 0: it takes the new one without a rescale
         const bool res = ref != old && old != neg_inf();
@@ -648,6 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
             uint32_t o[16];
             tmem_ld16(oc + c0, o);
             tmem_wait_ld();
+            after_wait<16>(o);
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = f2u(u2f(o[e]) * alpha);
             tmem_st16(oc + c0, o);
@@ -731,33 +752,80 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       // l > 0 unless every listed key is past the end or has a logit of -inf; NaN stays
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float* part = reinterpret_cast<float*>(sK);
-#pragma unroll
-      for (int c0 = 0; c0 < DP; c0 += 32) {
-        constexpr int kLast = DP - (DP - 1) / 32 * 32;    // columns of the last step
-        uint32_t op[32];
-#pragma unroll
-        for (int c = 0; c < (c0 + 32 <= DP ? 32 : kLast); c += 16) tmem_ld16p(oaddr + c0 + c, op + c);
+      // 16-bit rows in the layout of the TMA store's boxes: [64-column block][row], 16-byte chunks XOR-swizzled by
+      // (row & 7); the 8 tail columns of D = 72 as plain 16-byte rows
+      const bool pack = p.split == 1 && !p.out_f32;
+      uint8_t* tile = sQ + (nq % C::kNQ) * C::kTileBytes;
+      // Rolled loops, 16 columns a time: this code runs once an item, and unrolled its instruction misses held up
+      // every warp of the SM for longer than the work takes (5,000 clk, against 2,000 here, at D = 128).
+      auto load16 = [&](int c0, uint32_t (&op)[16]) {
+        tmem_ld16(oaddr + c0, op);
         tmem_wait_ld();
-        if (c0 + 32 >= DP) {                              // all of O is read: hand it back
+        after_wait<16>(op);
+        if (c0 + 16 >= DP) {
           tc_fence_before();
-          mbar_arrive(&bars[C::bOFree]);
+          mbar_arrive(&bars[C::bOFree]);                  // all of O is read: the next item's first P V may go
         }
-        if (!valid) continue;
+      };
+      if (pack) {
+        const bool some = __any_sync(0xffffffffu, l == 0.f);
+#pragma unroll 1
+        for (int c0 = 0; c0 < DP; c0 += 16) {
+          uint32_t op[16], pk[8];
+          load16(c0, op);
+          if (some && l == 0.f)
 #pragma unroll
-        for (int c = 0; c < 32 && c0 + c < D; c += 8) {
-          float x[8];
-          if (p.split > 1) {
+            for (int e = 0; e < 16; ++e) op[e] = 0u;
 #pragma unroll
-            for (int e = 0; e < 8; e += 4)
-              *reinterpret_cast<float4*>(part + part_chunk<DP>(r, (c0 + c + e) / 4)) =
-                  make_float4(u2f(op[c + e]), u2f(op[c + e + 1]), u2f(op[c + e + 2]), u2f(op[c + e + 3]));
+          for (int e = 0; e < 16; e += 2) pk[e / 2] = pack16<F16>(u2f(op[e]) * inv, u2f(op[e + 1]) * inv);
+          uint8_t* at = tile + (c0 >> 6) * C::kBlk;
+          if (c0 < 64 * C::kN64) {
+            at += r * 128;
+            const int ch = (c0 >> 3) & 7;
+            *reinterpret_cast<uint4*>(at + ((ch ^ (r & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           } else {
+            *reinterpret_cast<uint4*>(at + r * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c0 = 0; c0 < DP; c0 += 16) {
+          uint32_t op[16];
+          load16(c0, op);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : u2f(op[c + e]) * inv;
-            store_out8<F16>(p, orow + c0 + c, x);
+          for (int c = 0; c < 16; c += 8) {
+            if (c0 + c >= D) break;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = u2f(op[c + e]);
+            if (p.split > 1) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 4)
+                *reinterpret_cast<float4*>(part + part_chunk<DP>(r, (c0 + c + e) / 4)) =
+                    make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            } else if (valid) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : x[e] * inv;
+              store_out8<F16>(p, orow + c0 + c, x);
+            }
           }
         }
       }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        const int r0 = r;                                 // the warp's first row; rows past Sq are not written
+        if (pack && r0 < it.rows) {
+          for (int c = 0; c < C::kN64; ++c)
+            tma_store_3d(&p.tmO, tile + c * C::kBlk + r0 * 128, 64 * c, it.q0 + r0, it.h);
+          if (C::kTail) tma_store_3d(&p.tmOt, tile + C::kN64 * C::kBlk + r0 * 16, 64 * C::kN64, it.q0 + r0, it.h);
+          bulk_commit();
+          bulk_wait_read();
+        }
+        mbar_arrive(&bars[C::bQEmpty + nq % C::kNQ]);
+      }
+      __syncwarp();
       if (p.split == 1 && valid) *lrow = l == 0.f ? neg_inf() : (m + lg2(l)) * kLn2;
       ++nq;
     }
