@@ -105,16 +105,37 @@ __device__ __forceinline__ uint2 narrow4<__half>(const float* x) {
   const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
-// 8 elements as two groups of 4; one 16-byte access where they are adjacent 16-bit elements
+// 8 elements as two groups of 4; one 16-byte access where they are adjacent 16-bit elements.
+// copy8 starts their copy into this lane's shared-memory slot, read8 takes them from there.
+template <int N>
+__device__ __forceinline__ void async_copy(void* smem, const void* at) {
+  if (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(at) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem)), "l"(at) : "memory");
+}
+__device__ __forceinline__ void async_copy_l1(void* smem, const void* at) {      // 16 bytes, kept in L1
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(at) : "memory");
+}
 template <typename T, bool SPLIT>
-__device__ __forceinline__ void load8(const T* at, int gap, typename Vec4<T>::type (&v)[2]) {
-  using V = typename Vec4<T>::type;
+__device__ __forceinline__ void copy8(uint8_t* slot, const T* at, int gap) {
   if (sizeof(T) == 2 && !SPLIT) {
-    *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(at));
+    async_copy<16>(slot, at);
   } else {
-    v[0] = __ldcs(reinterpret_cast<const V*>(at));
-    v[1] = __ldcs(reinterpret_cast<const V*>(at + gap));
+    async_copy<4 * sizeof(T)>(slot, at);
+    async_copy<4 * sizeof(T)>(slot + 4 * sizeof(T), at + gap);
   }
+}
+template <typename T>
+__device__ __forceinline__ void read8(const uint8_t* slot, float* x) {
+  using V = typename Vec4<T>::type;
+  V v[2];
+  if (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(slot);
+  } else {
+    v[0] = reinterpret_cast<const V*>(slot)[0];
+    v[1] = reinterpret_cast<const V*>(slot)[1];
+  }
+  widen4<T>(v[0], x);
+  widen4<T>(v[1], x + 4);
 }
 template <typename T, bool SPLIT>
 __device__ __forceinline__ void store8(T* at, int gap, const float* x) {
@@ -128,36 +149,52 @@ __device__ __forceinline__ void store8(T* at, int gap, const float* x) {
   }
 }
 
-// A warp owns a head and a run of consecutive tokens: all 128 of a tile, or, when
-// that would leave SMs idle, 1/wt of them (wt = 2, 4, 8 warps per head).  The
-// warps of a CTA take neighbouring heads, so that together they read whole
-// stretches of a token-major row (8 heads of 128: 2 KB) and write whole
-// stretches of a head; a CTA per head, reading one 256-byte piece of every
-// row, reached 0.63 of the HBM rate on 40 heads of 128.  The tokens'
-// rotation comes from L2 once per CTA and from L1 for its other heads.  LPR
-// lanes hold a row, 8 elements each.  An element's partner in its pair is
-// always in the same thread (HALVES: 4 elements from each half), so the row's
-// sum of squares is the only exchange, by shuffles.  A row is loaded whole before
-// it is stored, by the warp that stores it (in-place calls).  Block means: sums over a
-// lane's rows, then over the lanes of the same columns, then over the warps of
-// the head through shared memory, in a fixed order.
+// A warp owns neighbouring heads, 32/LPR of them (LPR lanes hold a row, 8 elements
+// each), and a run of consecutive tokens, which it walks one by one: all 128 of a
+// tile, or, when that would leave SMs idle, 1/wt of them (wt = 2, 4, 8 warps
+// per run of heads).  A step's rows lie side by side in a token-major input, and
+// share the token's rotation.  The warps of a CTA take neighbouring heads too, so
+// the rotation comes from L2 once per CTA and from L1 for its other warps.  Rows and
+// rotations come through rings of asynchronous copies, kDepth steps deep: with
+// two or four rows in registers the pass waited on memory at 4.6-4.8 TB/s,
+// whatever it computed, and with the rotation loaded one step ahead its latency,
+// which the CTA's warps meet together, cost 80 us of 400 on 40 heads of 128.
+// An element's partner in its pair is always in the same lane (HALVES: 4
+// elements from each half), so the row's sum of squares is the only exchange, by
+// shuffles.  A row is read before it is stored, by the lanes that store it
+// (in-place calls).  Block means: sums over a lane's tokens, then over the
+// warps of the head through shared memory, in a fixed order.
 constexpr int kNormThreads = 256, kNormWarps = kNormThreads / 32;
 
+template <typename TI, int LPR>
+struct NormSmem {
+  static constexpr int kDepth = sizeof(TI) == 4 ? 4 : 8;
+  static constexpr int kSlot = 8 * sizeof(TI);      // bytes of a lane's 8 elements
+  static constexpr int kRing = kDepth * 32 * kSlot; // a warp's rows
+  static constexpr int kTurn = kDepth * LPR * 32;   // a warp's rotations (32 bytes per lane of a row)
+  static constexpr int kPart = kNormWarps * 32 * 8 * 4;
+  static constexpr int kBytes = kPart + kNormWarps * (kRing + kTurn);
+  static_assert(kRing >= 32 * 8 * 4, "a ring holds a warp's sums");
+};
+
 template <typename TI, typename TO, int LPR, bool HALVES>
-__global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int kTok = 32 / LPR;                    // tokens of a step
-  constexpr int kBatch = sizeof(TI) == 4 ? 2 : 4;   // steps whose rows are loaded together
-  // sums of each warp's segments (64 tokens, or the warp's run if shorter)
-  __shared__ float part[2 * kNormWarps][LPR * 8];
+__global__ void __launch_bounds__(kNormThreads, 3) qk_norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+  constexpr int kHeads = 32 / LPR;                  // heads of a warp
+  using M = NormSmem<TI, LPR>;
+  constexpr int kDepth = M::kDepth, kSlot = M::kSlot;
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  // Sums over each warp's first segment (64 tokens, or its run if shorter), then the rings; the sums over a second
+  // segment take the place of the warp's rows when all of those are read.
+  float* part = reinterpret_cast<float*>(norm_smem);
+  uint8_t* rings = norm_smem + M::kPart;
   const dt_norm_rope_params& p = a.p;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % LPR, sub = (threadIdx.x % 32) / LPR;
-  const int wh = kNormWarps / a.wt;                 // heads of the CTA
+  const int wh = kNormWarps / a.wt;                 // runs of heads of the CTA
   const int tile = blockIdx.x / a.groups, group = blockIdx.x - tile * a.groups;
   const int hw = warp / a.wt, ws = warp - hw * a.wt;
   const int run = 128 / a.wt, seg = min(run, 64);
-  const int hh = group * wh + hw;
-  const int s0 = tile * 128 + ws * run + sub;       // this lane's first token
-  const bool on = 8 * lane < p.D;
+  const int hh = (group * wh + hw) * kHeads + sub;  // this lane's head, counted over queries, keys, values
+  const int s0 = tile * 128 + ws * run;
   const bool turned = 8 * lane < p.rot;
   const int c0 = HALVES && turned ? 4 * lane : 8 * lane;
   const int gap = HALVES && turned ? p.rot / 2 : 4; // from the first 4 elements to the others
@@ -166,51 +203,77 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __g
   const int h = kind == 0 ? hh : (kind == 1 ? hh - p.H : hh - p.H - p.Hkv);
   const TI* in = static_cast<const TI*>(kind == 0 ? a.q : (kind == 1 ? a.k : a.v));
   TO* out = static_cast<TO*>(kind == 0 ? a.Q : (kind == 1 ? a.K : a.V));
-  float* mean = kind == 0 ? a.q_mean : (kind == 1 ? a.k_mean : nullptr);
-  if (hh < p.H + 2 * p.Hkv && in) {
-    const dt_strides si = kind == 0 ? p.q_in : (kind == 1 ? p.k_in : p.v_in);
-    const dt_strides so = kind == 0 ? p.q_out : (kind == 1 ? p.k_out : p.v_out);
-    const bool store = out != nullptr;
-    in += h * si.head + s0 * si.row + c0;
-    if (store) out += h * so.head + s0 * so.row + c0;
-    const int64_t istep = kTok * si.row, ostep = kTok * so.row;
-    int left = on ? p.S - s0 : 0;                   // rows from this lane's next to the end
-    const bool norm = kind < 2 && p.norm, turn = kind < 2 && turned;
-    const float* tr = a.table + ((int64_t)s0 * (p.rot / 2) + 4 * lane) * 2;
-    const int tstep = kTok * p.rot;
-    const float* w = kind == 0 ? a.wq : a.wk;
-    float wv[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    if (norm && w && on) {
-      widen(__ldg(reinterpret_cast<const float4*>(w + c0)), wv);
-      widen(__ldg(reinterpret_cast<const float4*>(w + c0 + gap)), wv + 4);
-    }
-    const uint64_t w2[4] = {pk2(wv[0], wv[1]), pk2(wv[2], wv[3]), pk2(wv[4], wv[5]), pk2(wv[6], wv[7])};
+  const bool on = 8 * lane < p.D && hh < p.H + 2 * p.Hkv && in;
+  int left = on ? min(p.S - s0, run) : 0;           // rows from this lane's next to the end of the run
+  const bool store = on && out != nullptr;
+  const dt_strides si = kind == 0 ? p.q_in : (kind == 1 ? p.k_in : p.v_in);
+  const dt_strides so = kind == 0 ? p.q_out : (kind == 1 ? p.k_out : p.v_out);
+  if (on) in += h * si.head + s0 * si.row + c0;
+  if (store) out += h * so.head + s0 * so.row + c0;
+  const bool turn = on && kind < 2 && turned;
+  const bool norm = p.norm && __any_sync(0xffffffffu, on && kind < 2);
+  const float* w = kind == 0 ? a.wq : a.wk;
+  float wv[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+  if (norm && w && on && kind < 2) {
+    widen(__ldg(reinterpret_cast<const float4*>(w + c0)), wv);
+    widen(__ldg(reinterpret_cast<const float4*>(w + c0 + gap)), wv + 4);
+  }
+  const uint64_t w2[4] = {pk2(wv[0], wv[1]), pk2(wv[2], wv[3]), pk2(wv[4], wv[5]), pk2(wv[6], wv[7])};
+  uint8_t* slot = rings + warp * M::kRing + (threadIdx.x % 32) * kSlot;       // a lane reads back what it copied
+  // A rotation row: lanes copy 16 bytes (two pairs) each; the two pieces of a reader's 4 pairs lie half a row apart,
+  // so that a read touches every bank once.
+  uint8_t* turns = rings + kNormWarps * M::kRing + warp * M::kTurn;
+  const int l32 = threadIdx.x % 32, tdst = ((l32 >> 1) + (l32 & 1) * LPR) * 16;
+  const bool any_turn = __any_sync(0xffffffffu, turn);
+  const float* tr = a.table + (int64_t)s0 * p.rot + 4 * l32;
+  int tleft = any_turn && 4 * l32 < p.rot ? min(p.S - s0, run) : 0;           // rotation rows left for this lane
+  // Lanes past D (or of no head) copy nothing: their slots are zero throughout, and add nothing to a row's sum.
+  // What a slot holds past the run's end is not stored and not summed.
+  if (!on)
+    for (int i = 0; i < kDepth; ++i)
+      for (int e = 0; e < kSlot; e += 16) *reinterpret_cast<uint4*>(slot + i * 32 * kSlot + e) = make_uint4(0, 0, 0, 0);
+  auto fetch = [&](int i, int ahead) {              // the row `ahead` tokens from this lane's next, into ring position i
+    if (ahead < left) copy8<TI, HALVES>(slot + i * 32 * kSlot, in, gap);
+    if (ahead < tleft) async_copy_l1(turns + i * LPR * 32 + tdst, tr);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    in += si.row;
+    tr += p.rot;
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch(i, i);
+  if (__all_sync(0xffffffffu, kind == 2)) {
+    // values: layout and type alone
+#pragma unroll 1
+    for (int t = 0; t < run; t += kDepth)
+#pragma unroll
+      for (int i = 0; i < kDepth; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        float x[8];
+        read8<TI>(slot + i * 32 * kSlot, x);
+        fetch((i + kDepth - 1) % kDepth, kDepth - 1);
+        if (left > 0 && store) store8<TO, HALVES>(out, gap, x);
+        out += so.row;
+        --left;
+      }
+  } else {
+    const bool sums = a.q_mean || a.k_mean;
 #pragma unroll 1
     for (int t0 = 0; t0 < run; t0 += seg) {
       uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
-      for (int t = 0; t < seg; t += kTok * kBatch) {
-        if (__all_sync(0xffffffffu, left <= 0)) break;
-        typename Vec4<TI>::type raw[kBatch][2];
+      for (int t = 0; t < seg; t += kDepth)
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          raw[b][0] = {};
-          raw[b][1] = {};
-          if (b * kTok < left) load8<TI, HALVES>(in, gap, raw[b]);
-          in += istep;
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const bool live = b * kTok < left;
-          float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
-          if (turn && live) {
-            u = __ldg(reinterpret_cast<const float4*>(tr));
-            v = __ldg(reinterpret_cast<const float4*>(tr) + 1);
-          }
-          tr += tstep;
+        for (int i = 0; i < kDepth; ++i) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+          __syncwarp();                             // every lane's copies have landed, and the slot refilled below is read
           float x[8];
-          widen4<TI>(raw[b][0], x);
-          widen4<TI>(raw[b][1], x + 4);
+          read8<TI>(slot + i * 32 * kSlot, x);
+          float4 c0v, c1v;                          // (cos, sin) of the lane's 4 pairs
+          if (turn) {
+            c0v = *reinterpret_cast<const float4*>(turns + i * LPR * 32 + lane * 16);
+            c1v = *reinterpret_cast<const float4*>(turns + i * LPR * 32 + LPR * 16 + lane * 16);
+          }
+          fetch((i + kDepth - 1) % kDepth, kDepth - 1);
           if (norm) {
             uint64_t x2[4] = {pk2(x[0], x[1]), pk2(x[2], x[3]), pk2(x[4], x[5]), pk2(x[6], x[7])};
             uint64_t ss2 = mul2(x2[0], x2[0]);
@@ -221,13 +284,14 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __g
             float ss = sa + sb;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = rsqrtf(fmaf(ss, a.inv_d, p.eps));
+            // a value head beside key heads keeps its scale
+            const float r = kind < 2 ? rsqrtf(fmaf(ss, a.inv_d, p.eps)) : 1.f;
             const uint64_t r2 = pk2(r, r);
 #pragma unroll
             for (int e = 0; e < 4; ++e) upk2(mul2(mul2(x2[e], r2), w2[e]), x[2 * e], x[2 * e + 1]);
           }
           if (turn) {
-            const float c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+            const float c[8] = {c0v.x, c0v.y, c0v.z, c0v.w, c1v.x, c1v.y, c1v.z, c1v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int ia = HALVES ? e : 2 * e, ib = HALVES ? e + 4 : 2 * e + 1;
@@ -236,50 +300,48 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __g
               x[ib] = fmaf(xa, c[2 * e + 1], xb * c[2 * e]);
             }
           }
-          if (live) {
+          if (left > 0) {
             if (store) store8<TO, HALVES>(out, gap, x);
+            if (sums)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], pk2(x[2 * e], x[2 * e + 1]));
+              for (int e = 0; e < 4; ++e) sum[e] = add2(sum[e], pk2(x[2 * e], x[2 * e + 1]));
           }
-          if (store) out += ostep;
+          out += so.row;
+          --left;
+          --tleft;
         }
-        left -= kTok * kBatch;
-      }
-      if (mean) {
+      if (sums) {
+        // (each lane overwrites its own slots, and every copy into them has been waited for or was never started)
+        if (t0 > 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if (t0 > 0) __syncwarp();
+        float* dst = (t0 > 0 ? reinterpret_cast<float*>(rings + warp * M::kRing) : part + warp * 256) + 8 * l32;
         float v[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) upk2(sum[e], v[2 * e], v[2 * e + 1]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-#pragma unroll
-          for (int o = LPR; o < 32; o <<= 1) v[e] += __shfl_xor_sync(0xffffffffu, v[e], o);
-        }
-        if (sub == 0) {
-          float* dst = &part[2 * warp + (t0 > 0)][8 * lane];
-          *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
   }
   if (!a.q_mean && !a.k_mean) return;
   __syncthreads();
   // one thread per (head of the CTA, 64-token half, column); a 128-row block is written by its first half
-  for (int i = threadIdx.x; i < wh * 2 * LPR * 8; i += kNormThreads) {
+  for (int i = threadIdx.x; i < wh * kHeads * 2 * LPR * 8; i += kNormThreads) {
     const int hi = i / (2 * LPR * 8), b = (i / (LPR * 8)) & 1, c = i % (LPR * 8);   // c: lane-major position
-    const int hq = group * wh + hi;
+    const int hq = group * wh * kHeads + hi, hr = hi / kHeads;
     float* m = hq < p.H ? a.q_mean : (hq < p.H + p.Hkv ? a.k_mean : nullptr);
     if (!m || !(hq < p.H ? a.q : a.k)) continue;
     const int blk = hq < p.H ? p.q_block : p.k_block, nblk = (p.S + blk - 1) / blk;
     const int r0 = tile * 128 + 64 * b, n = min(blk, p.S - r0);
     const int l8 = c / 8, e = c & 7;
     if ((blk == 128 && b == 1) || n <= 0 || 8 * l8 >= p.D) continue;
-    // the slots of half b: with one warp per head its segments b, else the warps of that half, segment 0 of each
+    // the slots of half b: with one warp per run of heads its segments, else the warps of that half, segment 0 of each
+    const int at = (hi % kHeads) * LPR * 8 + c;
     float v = 0.f;
     for (int hb = b; hb < (blk == 128 ? 2 : b + 1); ++hb) {
-      if (a.wt == 1) v += part[2 * hi + hb][c];
+      if (a.wt == 1) v += hb ? reinterpret_cast<const float*>(rings + hr * M::kRing)[at] : part[hr * 256 + at];
       else
-        for (int k = 0; k < a.wt / 2; ++k) v += part[2 * (hi * a.wt + hb * (a.wt / 2) + k)][c];
+        for (int k = 0; k < a.wt / 2; ++k) v += part[(hr * a.wt + hb * (a.wt / 2) + k) * 256 + at];
     }
     const bool tl = HALVES && 8 * l8 < p.rot;
     const int col = tl ? (e < 4 ? 4 * l8 + e : p.rot / 2 + 4 * l8 + e - 4) : 8 * l8 + e;
@@ -287,15 +349,20 @@ __global__ void __launch_bounds__(kNormThreads, 4) qk_norm_rope_kernel(const __g
   }
 }
 
+template <typename TI, typename TO, int LPR, bool HALVES>
+int norm_rope_launch(const NormRopeArgs& a, unsigned grid, cudaStream_t st) {
+  constexpr int kBytes = NormSmem<TI, LPR>::kBytes;
+  if (cudaFuncSetAttribute(qk_norm_rope_kernel<TI, TO, LPR, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kBytes) != cudaSuccess)
+    return DT_ERR_CUDA;
+  qk_norm_rope_kernel<TI, TO, LPR, HALVES><<<grid, kNormThreads, kBytes, st>>>(a);
+  return launched();
+}
 template <typename TI, typename TO>
-void norm_rope_dispatch(const NormRopeArgs& a, unsigned grid, cudaStream_t st) {
+int norm_rope_dispatch(const NormRopeArgs& a, unsigned grid, cudaStream_t st) {
   const bool hv = a.p.pairing == DT_ROPE_HALVES;
-#define DT_NR(LPR)                                                                                   \
-  (hv ? qk_norm_rope_kernel<TI, TO, LPR, true><<<grid, kNormThreads, 0, st>>>(a)                      \
-      : qk_norm_rope_kernel<TI, TO, LPR, false><<<grid, kNormThreads, 0, st>>>(a))
-  if (a.p.D <= 64) DT_NR(8);
-  else DT_NR(16);
-#undef DT_NR
+  if (a.p.D <= 64) return hv ? norm_rope_launch<TI, TO, 8, true>(a, grid, st) : norm_rope_launch<TI, TO, 8, false>(a, grid, st);
+  return hv ? norm_rope_launch<TI, TO, 16, true>(a, grid, st) : norm_rope_launch<TI, TO, 16, false>(a, grid, st);
 }
 
 // ------------------------------------------------------------------ block selection
@@ -313,7 +380,7 @@ void norm_rope_dispatch(const NormRopeArgs& a, unsigned grid, cudaStream_t st) {
 // pass from the highest bit in which the row's keys differ (order-preserving
 // 64-bit keys), ending as soon as a digit's keys are all wanted, and writes the
 // chosen blocks in increasing order by ballots.
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 
 // order-preserving key of a score; NaN counts as -infinity
 __device__ __forceinline__ uint64_t order_key(double x) {
@@ -400,6 +467,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_s
     uint64_t floor_key = 0;
     if (p.margin < INFINITY && nk > 0) {
       uint64_t best = 0;
+#pragma unroll 4
       for (int i = lane; i < nk; i += 32) best = max(best, kr[i]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) best = max(best, (uint64_t)__shfl_xor_sync(0xffffffffu, best, o));
@@ -407,6 +475,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_s
       floor_key = order_key(__longlong_as_double(b) - p.margin);
     }
     uint64_t all_and = ~0ull, all_or = 0;
+#pragma unroll 4
     for (int i = lane; i < nk; i += 32) {
       uint64_t k = kr[i];
       if (i < lo_keep || i >= hi_keep) kr[i] = k = forced;
@@ -431,6 +500,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_s
       shift -= bits;
       for (int i = lane; i < 256; i += 32) hs[i] = 0;
       __syncwarp();
+#pragma unroll 4
       for (int i = lane; i < nk; i += 32) {
         const uint64_t k = kr[i];
         if ((k & hi) == prefix) atomicAdd(&hs[(uint32_t)(k >> shift) & ((1u << bits) - 1u)], 1u);
@@ -465,6 +535,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_s
     int32_t* out = idx + ((int64_t)h * p.nq + q0 + r) * p.topk;
     const uint64_t open = shift == 64 ? 0ull : ~0ull << shift;
     int n = 0, eq = 0;
+#pragma unroll 2
     for (int i0 = 0; i0 < nk && topk > 0; i0 += 32) {
       const int i = i0 + lane;
       const uint64_t k = i < nk ? kr[i] : 0, kp = k & open;
@@ -509,19 +580,20 @@ int launch_qk_norm_rope(NormRopeArgs a, int sms, cudaStream_t stream) {
   const dt_norm_rope_params& p = a.p;
   const int64_t tiles = cdiv(p.S, 128);
   const int heads = p.H + 2 * p.Hkv;
-  // warps per head and tile: one, or more while the CTAs are fewer than two per SM
+  const int runs = cdiv(heads, p.D <= 64 ? 4 : 2);           // a warp's heads: 32 lanes / lanes per row
+  // warps per run of heads: one, or more while the CTAs are fewer than two per SM
   a.wt = 1;
-  while (a.wt < kNormWarps && tiles * cdiv(heads * a.wt, kNormWarps) < 2 * sms) a.wt *= 2;
-  a.groups = cdiv(heads * a.wt, kNormWarps);
+  while (a.wt < kNormWarps && tiles * cdiv(runs * a.wt, kNormWarps) < 2 * sms) a.wt *= 2;
+  a.groups = cdiv(runs * a.wt, kNormWarps);
   a.inv_d = 1.f / (float)p.D;
   if (tiles * a.groups >= (int64_t)1 << 31) return DT_ERR_INVALID;
   const unsigned grid = (unsigned)(tiles * a.groups);
-  if (p.in_type == DT_TYPE_BF16) norm_rope_dispatch<__nv_bfloat16, __nv_bfloat16>(a, grid, stream);
-  else if (p.in_type == DT_TYPE_F16 && p.out_type == DT_TYPE_F16) norm_rope_dispatch<__half, __half>(a, grid, stream);
-  else if (p.in_type == DT_TYPE_F16) norm_rope_dispatch<__half, __nv_bfloat16>(a, grid, stream);
-  else if (p.out_type == DT_TYPE_F32) norm_rope_dispatch<float, float>(a, grid, stream);
-  else norm_rope_dispatch<float, __nv_bfloat16>(a, grid, stream);
-  return launched();
+  if (p.in_type == DT_TYPE_BF16) return norm_rope_dispatch<__nv_bfloat16, __nv_bfloat16>(a, grid, stream);
+  if (p.in_type == DT_TYPE_F16)
+    return p.out_type == DT_TYPE_F16 ? norm_rope_dispatch<__half, __half>(a, grid, stream)
+                                     : norm_rope_dispatch<__half, __nv_bfloat16>(a, grid, stream);
+  return p.out_type == DT_TYPE_F32 ? norm_rope_dispatch<float, float>(a, grid, stream)
+                                   : norm_rope_dispatch<float, __nv_bfloat16>(a, grid, stream);
 }
 
 int launch_block_select(const dt_select_params& p, const float* q_mean, const float* k_mean, int32_t* idx,
