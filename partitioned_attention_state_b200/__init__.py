@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -98,6 +99,10 @@ class SelectParams(ctypes.Structure):
 class SparseParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("H", "Hkv", "Sq", "Sk", "D", "k_block", "cap", "type", "out_type")] + \
                [(n, Strides) for n in ("q", "k", "v", "o")]
+
+
+# the two structures above as packed fields
+_NORM_ROPE, _SPARSE = struct.Struct("@11if12q"), struct.Struct("@9i8q")
 
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -473,10 +478,13 @@ def norm_rope_params(q=None, k=None, v=None, Q=None, K=None, V=None, rot: int = 
     kv = k if k is not None else v
     _, S, D = first.shape
     ity = _type_of(first)
-    return NormRopeParams(S, D, 0 if q is None else q.shape[0], 0 if kv is None else kv.shape[0], rot, pairing, ity,
-                          ity if out is None else _type_of(out), int(norm), q_block, k_block, eps,
-                          *[(0, 0) if t is None else _heads(t, n) for n, t in
-                            (("q", q), ("k", k), ("v", v), ("Q", Q), ("K", K), ("V", V))])
+    strides = []
+    for n, t in (("q", q), ("k", k), ("v", v), ("Q", Q), ("K", K), ("V", V)):
+        strides += (0, 0) if t is None else _heads(t, n)
+    # packed in one go: setting the fields one by one costs as much as the launch
+    return NormRopeParams.from_buffer_copy(_NORM_ROPE.pack(
+        S, D, 0 if q is None else q.shape[0], 0 if kv is None else kv.shape[0], rot, pairing, ity,
+        ity if out is None else _type_of(out), int(norm), q_block, k_block, eps, *strides))
 
 
 def dt_qk_norm_rope(p: NormRopeParams, q, k, v, wq, wk, table, Q, K, V, q_mean=None, k_mean=None, stream=None) -> None:
@@ -490,22 +498,31 @@ def dt_qk_norm_rope(p: NormRopeParams, q, k, v, wq, wk, table, Q, K, V, q_mean=N
     dev, S, D, rot = first.get_device(), p.S, p.D, p.rot
     qs, ks, ity, oty = (p.H, S, D), (p.Hkv, S, D), _TYPES.get(p.in_type), _TYPES.get(p.out_type)
     ptr = []
-    for t, shape, n, ty in ((q, qs, "q_in", ity), (k, ks, "k_in", ity), (v, ks, "v_in", ity)):
-        if t is not None:
-            _match_heads(t, shape, getattr(p, n), ty, n, dev)
-        ptr.append(None if t is None else t.data_ptr())
+    for t, shape, st, n, ty in ((q, qs, p.q_in, "q", ity), (k, ks, p.k_in, "k", ity), (v, ks, p.v_in, "v", ity)):
+        if t is None:
+            ptr.append(None)
+        else:
+            _match_heads(t, shape, st, ty, n, dev)
+            ptr.append(t.data_ptr())
     for t, shape, n in ((wq, (D,), "wq"), (wk, (D,), "wk"), (table if rot else None, (S, rot // 2, 2), "table")):
-        if t is not None:
+        if t is None:
+            ptr.append(None)
+        else:
             _match(t, shape, f32, n, dev)
-        ptr.append(None if t is None else t.data_ptr())
-    for t, shape, n in ((Q, qs, "q_out"), (K, ks, "k_out"), (V, ks, "v_out")):
-        if t is not None:
-            _match_heads(t, shape, getattr(p, n), oty, n, dev)
-        ptr.append(None if t is None else t.data_ptr())
+            ptr.append(t.data_ptr())
+    for t, shape, st, n, ty in ((Q, qs, p.q_out, "Q", oty), (K, ks, p.k_out, "K", oty), (V, ks, p.v_out, "V", oty)):
+        if t is None:
+            ptr.append(None)
+        else:
+            _match_heads(t, shape, st, ty, n, dev)
+            ptr.append(t.data_ptr())
     for t, heads, block, n in ((q_mean, p.H, p.q_block, "q_mean"), (k_mean, p.Hkv, p.k_block, "k_mean")):
-        if t is not None and block > 0:
-            _match(t, (heads, -(-S // block), D), f32, n, dev)
-        ptr.append(None if t is None else t.data_ptr())
+        if t is None:
+            ptr.append(None)
+        else:
+            if block > 0:
+                _match(t, (heads, -(-S // block), D), f32, n, dev)
+            ptr.append(t.data_ptr())
     _call("dt_qk_norm_rope", dev, stream, p, *ptr)
 
 
@@ -532,8 +549,9 @@ def sparse_params(Q, K, V, O, k_block: int = 64, cap: int = 0) -> SparseParams:
     _init()
     H, Sq, D = Q.shape
     Hkv, Sk, _ = K.shape
-    return SparseParams(H, Hkv, Sq, Sk, D, k_block, cap, _type_of(Q), _type_of(O), _heads(Q, "Q"), _heads(K, "K"),
-                        _heads(V, "V"), _heads(O, "O"))
+    return SparseParams.from_buffer_copy(_SPARSE.pack(H, Hkv, Sq, Sk, D, k_block, cap, _type_of(Q), _type_of(O),
+                                                      *_heads(Q, "Q"), *_heads(K, "K"), *_heads(V, "V"),
+                                                      *_heads(O, "O")))
 
 
 def dt_attn_block_sparse(p: SparseParams, Q, K, V, idx, count, O, L, d_status, stream=None) -> None:

@@ -10,6 +10,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/dt.h"
 #include "sm100.cuh"
 #include "token_ops.h"
@@ -349,12 +351,22 @@ __global__ void __launch_bounds__(kNormThreads, 3) qk_norm_rope_kernel(const __g
   }
 }
 
+// Raises a kernel's shared-memory limit to `bytes`, once per device and size (racing threads repeat it harmlessly).
+template <typename K>
+bool allow_smem(K kernel, std::atomic<int> (&allowed)[64], int bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (allowed[dev].load(std::memory_order_acquire) >= bytes) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  allowed[dev].store(bytes, std::memory_order_release);
+  return true;
+}
+
 template <typename TI, typename TO, int LPR, bool HALVES>
 int norm_rope_launch(const NormRopeArgs& a, unsigned grid, cudaStream_t st) {
   constexpr int kBytes = NormSmem<TI, LPR>::kBytes;
-  if (cudaFuncSetAttribute(qk_norm_rope_kernel<TI, TO, LPR, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kBytes) != cudaSuccess)
-    return DT_ERR_CUDA;
+  static std::atomic<int> allowed[64];
+  if (!allow_smem(qk_norm_rope_kernel<TI, TO, LPR, HALVES>, allowed, kBytes)) return DT_ERR_CUDA;
   qk_norm_rope_kernel<TI, TO, LPR, HALVES><<<grid, kNormThreads, kBytes, st>>>(a);
   return launched();
 }
@@ -553,6 +565,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_s
   }
 }
 
+constexpr int kSelSmemMax = 160 * 1024;            // one row of DT_SELECT_MAX_BLOCKS keys and 8 of queries at D = 128
+
 size_t select_smem(int R, int D, int nk) {
   return ((size_t)(R > 8 ? 16 : 8) * select_ldq(D) + (size_t)R * nk) * 8;
 }
@@ -561,9 +575,9 @@ template <int MT>
 int select_launch(const dt_select_params& p, const float* qm, const float* km, int32_t* idx, int32_t* count, int R,
                   cudaStream_t st) {
   const size_t smem = select_smem(R, p.D, p.nk);
-  if (cudaFuncSetAttribute(block_select_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return DT_ERR_CUDA;
+  // the most that any call asks for, so that calls of other sizes never lower it under a call in flight
+  static std::atomic<int> allowed[64];
+  if (!allow_smem(block_select_kernel<MT>, allowed, kSelSmemMax)) return DT_ERR_CUDA;
   const int qtiles = cdiv(p.nq, R);
   block_select_kernel<MT><<<(unsigned)(p.H * qtiles), kSelThreads, smem, st>>>(p, qm, km, idx, count, qtiles, R);
   return launched();
