@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     // a Q buffer is free when its last Q K^T is done and the 4 epilogue warps have stored O from it
     for (int i = 0; i < C::kNQ; ++i) mbar_init(&bars[C::bQEmpty + i], 1 + 4);
     mbar_init(&bars[C::bOFree], 4 * 32);
-    // readers of an item: TMA thread, two MMA warps, softmax, epilogue
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[C::bInfoFree + i], 1 + 2 * 32 + 8 * 32 + 4 * 32);
+    // readers of an item: TMA and two MMA warps, softmax, epilogue
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[C::bInfoFree + i], 3 * 32 + 8 * 32 + 4 * 32);
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async();
@@ -394,7 +394,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       }
     } else if (warp == kWarpTma) {
       // ---------------------------------------------------------- TMA producer
-      if (lane == 0) {
+      // Whole-warp loops with an elected lane for the copies, as in the MMA warps: issued by one lane of a divergent
+      // loop, a tile's 8 copies took ~850 clk, and the loads ran no tile ahead of the tensor cores.
+      if (elect_one()) {
         prefetch_tmap(&p.tmQ);
         prefetch_tmap(&p.tmK);
         prefetch_tmap(&p.tmV);
@@ -403,86 +405,92 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
           prefetch_tmap(&p.tmKt);
           prefetch_tmap(&p.tmVt);
         }
-        // K/V blocks are read by many query blocks of the head; a Q tile once
-        const uint64_t pol_keep = l2_policy_evict_last(), pol_once = l2_policy_evict_first();
-        uint32_t gk = 0, gv = 0, nq = 0;                  // K tiles, V tiles, Q tiles issued
-        // 64 rows from row0 of a K, V or Q head, into half `half` of a tile
-        auto load_half = [&](const CUtensorMap* t64, const CUtensorMap* t16, uint8_t* tile, uint64_t* bar, int half,
-                             int row0, int h, uint64_t pol) {
+      }
+      __syncwarp();
+      // K/V blocks are read by many query blocks of the head; a Q tile once
+      const uint64_t pol_keep = l2_policy_evict_last(), pol_once = l2_policy_evict_first();
+      uint32_t gk = 0, gv = 0, nq = 0;                    // K tiles, V tiles, Q tiles issued
+      // 64 rows from row0 of a K, V or Q head, into half `half` of a tile
+      auto load_half = [&](const CUtensorMap* t64, const CUtensorMap* t16, uint8_t* tile, uint64_t* bar, int half,
+                           int row0, int h, uint64_t pol) {
 #pragma unroll
-          for (int c = 0; c < C::kN64; ++c)
-            tma_load_3d_hint(tile + c * C::kBlk + half * (C::kBlk / 2), t64, bar, 64 * c, row0, h, pol);
-          if (C::kTail)
-            tma_load_3d_hint(tile + C::kN64 * C::kBlk + half * (C::kTailBytes / 2), t16, bar, 64 * C::kN64, row0, h, pol);
-        };
-        Halves vp = {0, 0};                               // the tile whose V is still to be issued
-        int vh = -1;
-        auto issue_v = [&]() {
-          if (vh < 0) return true;
-          const uint32_t st = gv % C::kNV;
-          if (gv >= (uint32_t)C::kNV &&
-              !thread_wait(&bars[C::bVEmpty + st], ((gv / C::kNV) - 1) & 1, abort_flag, p.status, lim))
-            return false;
+        for (int c = 0; c < C::kN64; ++c)
+          tma_load_3d_hint(tile + c * C::kBlk + half * (C::kBlk / 2), t64, bar, 64 * c, row0, h, pol);
+        if (C::kTail)
+          tma_load_3d_hint(tile + C::kN64 * C::kBlk + half * (C::kTailBytes / 2), t16, bar, 64 * C::kN64, row0, h, pol);
+      };
+      Halves vp = {0, 0};                                 // the tile whose V is still to be issued
+      int vh = -1;
+      auto issue_v = [&]() {
+        if (vh < 0) return true;
+        const uint32_t st = gv % C::kNV;
+        if (gv >= (uint32_t)C::kNV && !warp_wait(&bars[C::bVEmpty + st], ((gv / C::kNV) - 1) & 1, abort_flag, p.status, lim))
+          return false;
+        if (elect_one()) {
           uint8_t* dst = sV + st * C::kTileBytes;
           uint64_t* full = &bars[C::bVFull + st];
           mbar_arrive_expect_tx(full, vp.r1 < 0 ? C::kTileBytes / 2 : C::kTileBytes);
           load_half(&p.tmV, &p.tmVt, dst, full, 0, vp.r0, vh, pol_keep);
           if (vp.r1 >= 0) load_half(&p.tmV, &p.tmVt, dst, full, 1, vp.r1, vh, pol_keep);
-          vh = -1;
-          ++gv;
-          return true;
-        };
-        // V(g) goes out after K(g+1): the order in which their stages fall free
-        for (uint32_t seq = 0;; ++seq) {
-          uint64_t* ready = &bars[C::bInfoFull + (seq & 1)];
-          if (!mbar_test(ready, (seq >> 1) & 1) &&
-              (!issue_v() || !thread_wait(ready, (seq >> 1) & 1, abort_flag, p.status, lim)))
-            break;
-          const Item it = info[seq & 1];
-          mbar_arrive(&bars[C::bInfoFree + (seq & 1)]);
-          if (it.h < 0) break;
-          if (it.nt == 0) continue;
-          const uint32_t b = nq % C::kNQ;
-          if (nq >= (uint32_t)C::kNQ &&
-              !thread_wait(&bars[C::bQEmpty + b], (nq / C::kNQ - 1) & 1, abort_flag, p.status, lim))
-            goto tma_done;
+        }
+        __syncwarp();
+        vh = -1;
+        ++gv;
+        return true;
+      };
+      // V(g) goes out after K(g+1): the order in which their stages fall free
+      bool ok = true;
+      Item it;
+      for (uint32_t seq = 0; ok; ++seq) {
+        // the last V of an item goes first if the next item is not there yet
+        if (!__all_sync(0xffffffffu, mbar_test(&bars[C::bInfoFull + (seq & 1)], (seq >> 1) & 1))) ok = issue_v();
+        if (!ok || !next_item(seq, it)) break;
+        if (it.nt == 0) continue;
+        const uint32_t b = nq % C::kNQ;
+        ok = nq < (uint32_t)C::kNQ ||
+             warp_wait(&bars[C::bQEmpty + b], (nq / C::kNQ - 1) & 1, abort_flag, p.status, lim);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&bars[C::bQFull + b], C::kTileBytes);
           load_half(&p.tmQ, &p.tmQt, sQ + b * C::kTileBytes, &bars[C::bQFull + b], 0, it.q0, it.h, pol_once);
           load_half(&p.tmQ, &p.tmQt, sQ + b * C::kTileBytes, &bars[C::bQFull + b], 1, it.q0 + 64, it.h, pol_once);
-          ++nq;
-          const int hk = it.h / p.per_kv;
-          Entries nxt = {it.first_a, it.first_b};
-          for (int t = it.t0; t < it.t0 + it.nt; ++t) {
-            const Halves v = tile_halves(p, it, t, nxt);
-            if (t + 1 < it.t0 + it.nt) nxt = load_entries(p, it, t + 1);
-            const uint32_t st = gk % C::kNK;
-            if (gk >= (uint32_t)C::kNK &&
-                !thread_wait(&bars[C::bKEmpty + st], ((gk / C::kNK) - 1) & 1, abort_flag, p.status, lim))
-              goto tma_done;
+        }
+        __syncwarp();
+        ++nq;
+        const int hk = (int)((unsigned)it.h / (unsigned)p.per_kv);
+        Entries nxt = {it.first_a, it.first_b};
+        for (int t = it.t0; ok && t < it.t0 + it.nt; ++t) {
+          const Halves v = tile_halves(p, it, t, nxt);
+          if (t + 1 < it.t0 + it.nt) nxt = load_entries(p, it, t + 1);
+          const uint32_t st = gk % C::kNK;
+          ok = gk < (uint32_t)C::kNK ||
+               warp_wait(&bars[C::bKEmpty + st], ((gk / C::kNK) - 1) & 1, abort_flag, p.status, lim);
+          if (!ok) break;
+          if (elect_one()) {
             uint8_t* dst = sK + st * C::kTileBytes;
             uint64_t* full = &bars[C::bKFull + st];
             mbar_arrive_expect_tx(full, v.r1 < 0 ? C::kTileBytes / 2 : C::kTileBytes);
             load_half(&p.tmK, &p.tmKt, dst, full, 0, v.r0, hk, pol_keep);
             if (v.r1 >= 0) load_half(&p.tmK, &p.tmKt, dst, full, 1, v.r1, hk, pol_keep);
-            ++gk;
-            if (!issue_v()) goto tma_done;
-            vp = v;
-            vh = hk;
           }
+          __syncwarp();
+          ++gk;
+          ok = issue_v();
+          vp = v;
+          vh = hk;
         }
-        issue_v();
-      tma_done:
-        // let every copy this thread started land before shared memory goes away
-        volatile int never = 0;
-        auto drain = [&](int bar, uint32_t stages, uint32_t n) {
-          for (uint32_t s = 0; s < stages; ++s)
-            if (s < n)                                    // the latest tile that used stage s
-              thread_wait(&bars[bar + s], ((n - 1 - ((n - 1 - s) % stages)) / stages) & 1, &never, p.status, kDrainLimitNs);
-        };
-        drain(C::bKFull, C::kNK, gk);
-        drain(C::bVFull, C::kNV, gv);
-        drain(C::bQFull, C::kNQ, nq);
       }
+      if (ok) issue_v();
+      // let every copy this warp started land before shared memory goes away
+      volatile int never = 0;
+      auto drain = [&](int bar, uint32_t stages, uint32_t n) {
+        for (uint32_t s = 0; s < stages; ++s)
+          if (s < n)                                      // the latest tile that used stage s
+            warp_wait(&bars[bar + s], ((n - 1 - ((n - 1 - s) % stages)) / stages) & 1, &never, p.status, kDrainLimitNs);
+      };
+      drain(C::bKFull, C::kNK, gk);
+      drain(C::bVFull, C::kNV, gv);
+      drain(C::bQFull, C::kNQ, nq);
       __syncwarp();
     } else if (warp == kWarpMma) {
       // ---------------------------------------------------------- S = Q K^T
