@@ -13,7 +13,7 @@
 //
 // A work item is (head, query block), and the grid has a CTA per item.  With at
 // least as many items as SMs, a running CTA takes further items over from CTAs
-// that have not started (cluster launch control), an item ahead of its need: the
+// that have not started (cluster launch control), a few tiles ahead of its need: the
 // lists may have any lengths, and this balances them without a counter in
 // memory, keeps the items head-major, so that CTAs that run together read one
 // head's K and V through L2, and overlaps one item's end with the next one's
@@ -76,6 +76,7 @@ constexpr uint64_t kDrainLimitNs = 1000000000ull;
 constexpr int kMaxDevices = 64;
 constexpr int kMaxSplit = 16;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kLead = 8;                    // tiles of an item left to load when the next item is taken
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale O only when the max grows by > 2^8
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
@@ -101,7 +102,7 @@ struct Cfg {
                        bKEmpty = bVFull + kNV, bVEmpty = bKEmpty + kNK, bSFull = bVEmpty + kNV,
                        bPFull = bSFull + kNS, bPVDone = bPFull + kNS, bOFull = bPVDone + kNS, bOFree = bOFull + 1,
                        bStFull = bOFree + 1, bStFree = bStFull + 1, bTok = bStFree + 1, bInfoFull = bTok + 8,
-                       bInfoFree = bInfoFull + 2, bClc = bInfoFree + 2, bDrain = bClc + 1, bDrainPV = bDrain + 1,
+                       bInfoFree = bInfoFull + 2, bNeed = bInfoFree + 2, bClc = bNeed + 1, bDrain = bClc + 1, bDrainPV = bDrain + 1,
                        kNumBars = bDrainPV + 1 + (bDrainPV & 1 ? 0 : 1);      // even: what follows is 16-byte aligned
   // per row: reference maximum, and each set's (maximum, sum) of the item
   static constexpr int kStatsBytes = 5 * 128 * 4;
@@ -341,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     // a Q buffer is free when its last Q K^T is done and the 4 epilogue warps have stored O from it
     for (int i = 0; i < C::kNQ; ++i) mbar_init(&bars[C::bQEmpty + i], 1 + 4);
     mbar_init(&bars[C::bOFree], 4 * 32);
+    mbar_init(&bars[C::bNeed], 32);
     // readers of an item: TMA and two MMA warps, softmax, epilogue
     for (int i = 0; i < 2; ++i) mbar_init(&bars[C::bInfoFree + i], 3 * 32 + 8 * 32 + 4 * 32);
     *abort_flag = 0;
@@ -367,30 +369,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
     regs_set<kLaunchRegs, kRegsOther>();
     if (warp == kWarpSched) {
       // ---------------------------------------------------------- scheduler
+      // An item is taken when the TMA warp has kLead tiles of the one before left to issue: late enough that a CTA
+      // hoards nothing (taken two items ahead, ragged lists of 3.5 items a CTA ended 20 % later), early enough for
+      // the answer and the list's two memory latencies.
       const uint32_t answer = smem_u32(clc);
       int item = blockIdx.x / p.split;
-      for (uint32_t seq = 0;; ++seq) {
-        const bool ask = item >= 0 && p.split == 1;       // the item after this one
-        if (ask && lane == 0) clc_ask(answer, &bars[C::bClc]);
+      bool ok = true;
+      for (uint32_t seq = 0; ok; ++seq) {
+        if (seq > 0 && p.split > 1) item = -1;
+        if (seq > 0 && p.split == 1) {
+          ok = warp_wait(&bars[C::bNeed], (seq - 1) & 1, abort_flag, p.status, lim);
+          if (!ok) break;
+          if (lane == 0) clc_ask(answer, &bars[C::bClc]);
+          __syncwarp();
+          volatile int never = 0;                         // waited for whatever happens: the answer is in flight
+          ok = warp_wait(&bars[C::bClc], (seq - 1) & 1, &never, p.status, kDrainLimitNs);
+          if (!ok) break;
+          item = clc_answer(answer);
+          fence_proxy_async();                            // the answer is read before the next one overwrites it
+        }
         Item it = {};
         it.h = -1;
         if (item >= 0) it = make_item(p, item, rank, lane);
-        bool ok = seq < 2 || warp_wait(&bars[C::bInfoFree + (seq & 1)], ((seq >> 1) - 1) & 1, abort_flag, p.status, lim);
-        if (ok) {
-          if (lane == 0) {
-            info[seq & 1] = it;
-            mbar_arrive(&bars[C::bInfoFull + (seq & 1)]);
-          }
-          __syncwarp();
+        ok = seq < 2 || warp_wait(&bars[C::bInfoFree + (seq & 1)], ((seq >> 1) - 1) & 1, abort_flag, p.status, lim);
+        if (!ok) break;
+        if (lane == 0) {
+          info[seq & 1] = it;
+          mbar_arrive(&bars[C::bInfoFull + (seq & 1)]);
         }
-        if (ask) {                                        // waited for after an abort too: the answer is in flight
-          volatile int never = 0;
-          ok = __all_sync(0xffffffffu, thread_wait(&bars[C::bClc], seq & 1, &never, p.status, kDrainLimitNs)) && ok;
-        }
-        if (!ok || it.h < 0) break;
-        item = ask ? clc_answer(answer) : -1;
-        fence_proxy_async();                              // the answer is read before the next one overwrites it
         __syncwarp();
+        if (it.h < 0) break;
       }
     } else if (warp == kWarpTma) {
       // ---------------------------------------------------------- TMA producer
@@ -445,6 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         // the last V of an item goes first if the next item is not there yet
         if (!__all_sync(0xffffffffu, mbar_test(&bars[C::bInfoFull + (seq & 1)], (seq >> 1) & 1))) ok = issue_v();
         if (!ok || !next_item(seq, it)) break;
+        if (it.nt <= kLead) mbar_arrive(&bars[C::bNeed]);
         if (it.nt == 0) continue;
         const uint32_t b = nq % C::kNQ;
         ok = nq < (uint32_t)C::kNQ ||
@@ -475,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
           }
           __syncwarp();
           ++gk;
+          if (it.t0 + it.nt - t == kLead + 1) mbar_arrive(&bars[C::bNeed]);
           ok = issue_v();
           vp = v;
           vh = hk;
