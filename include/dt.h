@@ -413,16 +413,15 @@ typedef struct { int64_t head, row; } dt_strides;
 
 #define DT_ROPE_MAX_AXES 4
 typedef struct {
-  int32_t S;                    /* tokens */
+  int32_t S;                    /* tokens, at most 2^30 (here and below) */
   int32_t n_axes;               /* position axes, 1 .. DT_ROPE_MAX_AXES */
   int32_t dim[DT_ROPE_MAX_AXES];/* rotated dimensions of each axis: even, > 0, sum rot <= 256 */
-  double base;                  /* frequency base, > 0 (10000 is usual) */
+  double base;                  /* frequency base, >= 1 (10000 is usual) */
 } dt_rope_params;
 
 /* Rotation table: pair i of axis a (j-th pair of that axis, axes in order) of
  * token s turns by pos[a][s] * base^(-2 j / dim[a]); table[s][i] = (cos, sin).
- * Angles are formed and reduced in 64 bits, so far positions keep their
- * fraction.
+ * The fraction of a turn is formed in 64 bits, so far positions keep theirs.
  *   pos     int32 [n_axes][S] (device, read; any sign)
  *   table   fp32 [S][rot/2][2] (device, written)
  * One launch, HBM-bound.  S = 0 launches nothing.  Errors: DT_ERR_INVALID,
@@ -455,8 +454,8 @@ typedef struct {
  *   table       fp32 [S][rot/2][2] of dt_rope_table; not read with rot = 0
  *   Q, K, V     outputs with strides q_out, k_out, v_out.  Q and K may be
  *               NULL where their mean is wanted alone.  An output may be its
- *               own input in place (same pointer, strides and type); other
- *               overlaps are not allowed
+ *               own input in place (same pointer, strides and type, or
+ *               DT_ERR_INVALID); other overlaps are not allowed
  *   q_mean      fp32 [H][ceil(S/q_block)][D] or NULL: mean of each block of
  *               consecutive rows (the last block: of the rows it has), of the
  *               values before the rounding to out_type
@@ -524,7 +523,9 @@ typedef struct {
  * those of Q, K and V below 2^40 bytes.
  * With few query blocks the CTAs of a cluster split each list and join their
  * states through distributed shared memory: one launch, no workspace, and the
- * same result run to run.  Sq = 0 or H = 0 launches nothing.  Errors:
+ * same result run to run.  The waits of dt_set_wait_limit_ns span whole lists:
+ * a list of millions of tiles on one CTA (about 0.8 us per 128 keys) needs a
+ * limit above its time.  Sq = 0 or H = 0 launches nothing.  Errors:
  * DT_ERR_INVALID, DT_ERR_UNSUPPORTED (D, types, alignment), DT_ERR_CUDA;
  * DT_ERR_TIMEOUT and DT_ERR_INVALID through d_status. */
 DT_API int dt_attn_block_sparse(const dt_sparse_params* p, const void* Q, const void* K, const void* V,

@@ -352,8 +352,8 @@ bool encode_strided(CUtensorMap* m, const void* base, int heads, int S, int D, d
 }  // namespace
 
 extern "C" int dt_rope_table(const dt_rope_params* p, const int32_t* pos, float* table, void* stream) {
-  if (!p || p->S < 0 || p->n_axes < 1 || p->n_axes > DT_ROPE_MAX_AXES) return DT_ERR_INVALID;
-  if (!(p->base > 0.0) || !std::isfinite(p->base)) return DT_ERR_INVALID;
+  if (!p || p->S < 0 || p->S > 1 << 30 || p->n_axes < 1 || p->n_axes > DT_ROPE_MAX_AXES) return DT_ERR_INVALID;
+  if (!(p->base >= 1.0) || !std::isfinite(p->base)) return DT_ERR_INVALID;
   int64_t rot = 0;
   for (int a = 0; a < p->n_axes; ++a) {
     if (p->dim[a] < 2 || p->dim[a] % 2 != 0) return DT_ERR_INVALID;
@@ -407,6 +407,11 @@ extern "C" int dt_qk_norm_rope(const dt_norm_rope_params* p, const void* q, cons
       if (!strides_nonneg(x.s, x.heads, p->S)) return DT_ERR_INVALID;
       if (!aligned16(x.p) || !strides_aligned(x.s, x.heads, p->S, x.size)) return DT_ERR_UNSUPPORTED;
     }
+  // in place: each element is read and written by one thread only if both sides are laid out alike
+  for (int i = 0; i < 3; ++i)
+    if (t[i].p && t[i].p == t[i + 3].p &&
+        (p->in_type != p->out_type || t[i].s.row != t[i + 3].s.row || t[i].s.head != t[i + 3].s.head))
+      return DT_ERR_INVALID;
   for (const void* x : {(const void*)wq, (const void*)wk, (const void*)table, (const void*)q_mean, (const void*)k_mean})
     if (x && !aligned16(x)) return DT_ERR_UNSUPPORTED;
   if (p->S == 0 || p->H + p->Hkv == 0) return DT_OK;

@@ -88,7 +88,12 @@ class Session:
             self.last_anchored = False
         self.last_counts = None
         self.last_plan = None
-        self.q_mean = self.k_mean = None      # block means of the last set_projection or step_sparse
+        # block means and lists of sparse steps, one buffer per k_block and per topk, kept: a captured graph goes on
+        # using the ones it was captured with
+        self._means: dict = {}
+        self._lists: dict = {}
+        self._measured: Optional[int] = None  # k_block for which the means are those of the current Q and K
+        self.q_mean = self.k_mean = None      # means of the last set_projection or step_sparse
         self.lists = None                     # (idx, count) of the last step_sparse
 
     def _plan_buffers(self) -> None:
@@ -128,12 +133,14 @@ class Session:
                 dst.copy_(bf16_from_bits(src, "cpu"))
             else:
                 dst.copy_(src)
+        self._measured = None
 
-    def _means(self, k_block: int) -> None:
-        nq, nk = -(-self.S // DT_TILE), -(-self.S // k_block)
-        if self.k_mean is None or self.k_mean.shape[1] != nk:
-            self.q_mean = torch.empty((self.H, nq, self.D), dtype=torch.float32, device=self.device)
-            self.k_mean = torch.empty((self.H, nk, self.D), dtype=torch.float32, device=self.device)
+    def _use_means(self, k_block: int) -> None:
+        if k_block not in self._means:
+            self._means[k_block] = tuple(
+                torch.empty((self.H, -(-self.S // block), self.D), dtype=torch.float32, device=self.device)
+                for block in (DT_TILE, k_block))
+        self.q_mean, self.k_mean = self._means[k_block]
 
     def set_projection(self, qkv: torch.Tensor, wq=None, wk=None, table=None, pairing: int = DT_ROPE_INTERLEAVED,
                        norm: bool = True, eps: float = 1e-6, k_block: int = 64, stream=None) -> None:
@@ -146,10 +153,13 @@ class Session:
         if tuple(qkv.shape) != (self.S, 3 * self.H * self.D):
             raise ValueError(f"qkv: expected {(self.S, 3 * self.H * self.D)}, got {tuple(qkv.shape)}")
         x = qkv.unflatten(1, (3, self.H, self.D)).permute(1, 2, 0, 3)
-        self._means(k_block)
+        if k_block not in (64, 128):
+            raise ValueError(f"k_block: 64 or 128, got {k_block}")
+        self._use_means(k_block)
         p = norm_rope_params(x[0], x[1], x[2], self.Q, self.K, self.V, rot=0 if table is None else 2 * table.shape[1],
                              pairing=pairing, norm=norm, eps=eps, q_block=DT_TILE, k_block=k_block)
         dt_qk_norm_rope(p, x[0], x[1], x[2], wq, wk, table, self.Q, self.K, self.V, self.q_mean, self.k_mean, stream)
+        self._measured = k_block
 
     # -------------------------------------------------------------- planning
     def plan(self, step: int, mode: Optional[int] = None, explicit: Optional[np.ndarray] = None):
@@ -246,20 +256,22 @@ class Session:
         means that set_projection (same k_block) left, which is right as long as
         Q and K are what it wrote; else they are measured first.  The lists
         stay in ``lists`` (idx, count)."""
-        had = None if self.k_mean is None else self.k_mean.shape[1]
-        if not remeasure and had != -(-self.S // k_block):
+        if k_block not in (64, 128):
+            raise ValueError(f"k_block: 64 or 128, got {k_block}")
+        if not remeasure and self._measured != k_block:
             raise ValueError("remeasure=False needs the block means of set_projection with this k_block")
-        self._means(k_block)
+        self._use_means(k_block)
         if remeasure:
             p = norm_rope_params(self.Q, self.K, norm=False, q_block=DT_TILE, k_block=k_block)
             dt_qk_norm_rope(p, self.Q, self.K, None, None, None, None, None, None, None, self.q_mean, self.k_mean, stream)
+            self._measured = k_block
         nq, nk = self.q_mean.shape[1], self.k_mean.shape[1]
-        if self.lists is None or self.lists[0].shape != (self.H, nq, topk):
-            self.lists = (torch.empty((self.H, nq, topk), dtype=torch.int32, device=self.device),
-                          torch.empty((self.H, nq), dtype=torch.int32, device=self.device))
-        idx, count = self.lists
-        dt_block_select(select_params(self.H, self.H, nq, nk, self.D, topk, keep_first, keep_last, margin), self.q_mean,
-                        self.k_mean, idx, count, stream)
+        sel = select_params(self.H, self.H, nq, nk, self.D, topk, keep_first, keep_last, margin)
+        if topk not in self._lists:
+            self._lists[topk] = (torch.empty((self.H, nq, topk), dtype=torch.int32, device=self.device),
+                                 torch.empty((self.H, nq), dtype=torch.int32, device=self.device))
+        self.lists = idx, count = self._lists[topk]
+        dt_block_select(sel, self.q_mean, self.k_mean, idx, count, stream)
         dt_attn_block_sparse(sparse_params(self.Q, self.K, self.V, self.O, k_block, topk), self.Q, self.K, self.V, idx,
                              count, self.O, self.L, self.status, stream)
 
@@ -286,6 +298,7 @@ class Session:
         made to wait for, everything issued here: synchronise the current
         stream before reading o and lse.  Returns the plan counts."""
         dev = self.device
+        self._measured = None
         cur = torch.cuda.current_stream(dev)
         if getattr(self, "_host_streams", None) is None:
             self._host_streams = tuple(torch.cuda.Stream(dev) for _ in range(3))

@@ -45,6 +45,7 @@ def rope(S=4, axes=(8, 8), base=10000.0, pos=P, table=P, **over):
 
 @pytest.mark.parametrize("kw", [dict(S=-1), dict(axes=(7,)), dict(axes=(0,)), dict(axes=(-2,)), dict(axes=(200, 58)),
                                 dict(base=0.0), dict(base=-1.0), dict(base=float("nan")), dict(base=float("inf")),
+                                dict(base=0.99), dict(S=(1 << 30) + 1),
                                 dict(pos=None), dict(table=None), dict(n_axes=0), dict(n_axes=5)])
 def test_rope_table_refuses(kw):
     assert rope(**kw) == dt.DT_ERR_INVALID
@@ -96,6 +97,13 @@ def test_norm_rope_types_alignment_strides():
     assert norm_rope(S=0) == dt.DT_OK
     none = {n: None for n in NAMES}
     assert norm_rope(none) == dt.DT_OK                                          # no part at all
+
+
+def test_norm_rope_in_place_needs_the_same_layout():
+    one = {**{n: None for n in NAMES}, "q": P, "Q": P, "wq": P, "table": P}
+    assert norm_rope(one, in_type=2, out_type=0) == dt.DT_ERR_INVALID
+    assert norm_rope(one, strides=dict(q_out=dt.Strides(640, 128))) == dt.DT_ERR_INVALID
+    assert norm_rope(one, strides=dict(q_out=dt.Strides(1280, 64))) == dt.DT_ERR_INVALID
 
 
 # ------------------------------------------------------------------ selection

@@ -6,6 +6,9 @@ type is off by at most half a step (bf16 2^-8, fp16 2^-11 of the value, fp16
 below 2^-14 by 2^-25 absolutely), one to fp32 by 2^-24."""
 
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -18,6 +21,7 @@ from partitioned_attention_state_b200.session import Session
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BF, FP, F32 = torch.bfloat16, torch.float16, torch.float32
 HALF = {BF: 2.0 ** -8, FP: 2.0 ** -11, F32: 2.0 ** -24}
 TINY = {BF: 0.0, FP: 2.0 ** -25, F32: 0.0}
@@ -145,6 +149,43 @@ def test_norm_rope_one_token_into_a_longer_cache_and_in_place():
     dt.dt_qk_norm_rope(p, yq, yk, None, None, None, table, yq, yk, None)
     assert torch.equal(yq, Q) and torch.equal(yk, want[0][:, 211:212])
     assert torch.equal(y[:, 2 * H:], x[:, 2 * H:])
+
+
+@pytest.mark.parametrize("ty", [BF, FP, F32])
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("S,H,Hkv,D", [(1, 3, 1, 64), (333, 3, 3, 72), (2500, 24, 8, 128)])
+def test_norm_rope_in_place_equals_out_of_place(ty, halves, S, H, Hkv, D):
+    """Packed token-major tensors normalised over themselves, at sizes with one and with many warps per head."""
+    g = gen(S)
+    x = randn(g, S, H + 2 * Hkv, D, dtype=ty)
+    t = x.transpose(0, 1)
+    ang = torch.rand(S, D // 2, generator=g, device="cuda")
+    table = torch.stack([ang.cos(), ang.sin()], -1)
+    w = 1 + 0.1 * randn(g, D)
+    Q, K = torch.empty(H, S, D, dtype=ty, device="cuda"), torch.empty(Hkv, S, D, dtype=ty, device="cuda")
+    p = dt.norm_rope_params(t[:H], t[H:H + Hkv], None, Q, K, None, rot=D, pairing=int(halves))
+    dt.dt_qk_norm_rope(p, t[:H], t[H:H + Hkv], None, w, w, table, Q, K, None)
+    y = x.clone()
+    u = y.transpose(0, 1)
+    qm, km = torch.empty(H, -(-S // 128), D, device="cuda"), torch.empty(Hkv, -(-S // 64), D, device="cuda")
+    p = dt.norm_rope_params(u[:H], u[H:H + Hkv], None, u[:H], u[H:H + Hkv], None, rot=D, pairing=int(halves))
+    dt.dt_qk_norm_rope(p, u[:H], u[H:H + Hkv], None, w, w, table, u[:H], u[H:H + Hkv], None, qm, km)
+    assert torch.equal(u[:H], Q) and torch.equal(u[H:H + Hkv], K) and torch.equal(y[:, H + Hkv:], x[:, H + Hkv:])
+
+
+def test_norm_rope_odd_head_counts_mix_parts_in_a_warp():
+    """Heads of all parts share warps when the counts are odd; infinities in one head stay there."""
+    norm_case(130, 5, 3, 64, 64, False, BF, BF, seed=21)
+    norm_case(130, 1, 1, 128, 64, True, FP, FP, seed=22)
+    g = gen(23)
+    x = randn(g, 70, 5, 64, dtype=BF)
+    x[:, 1] = math.inf
+    t = x.transpose(0, 1)
+    q, k, v = t[:1], t[1:3], t[3:5]
+    Q, K, V = (torch.empty(n, 70, 64, dtype=BF, device="cuda") for n in (1, 2, 2))
+    p = dt.norm_rope_params(q, k, v, Q, K, V)
+    dt.dt_qk_norm_rope(p, q, k, v, None, None, None, Q, K, V)
+    assert bool(torch.isfinite(Q).all()) and bool(torch.isfinite(K[1]).all()) and torch.equal(V, v)
 
 
 def test_norm_rope_means_alone_and_single_parts():
@@ -362,6 +403,55 @@ def test_attention_token_major_views_and_longer_caches():
     O2, L2, _ = attend(q.contiguous(), k.contiguous(), v.contiguous(), idx, count, 64)
     assert st == 0 and torch.equal(O, O2) and torch.equal(L, L2)
     check_attention(q, k, v, idx, count, 64, O, L)
+
+
+def test_attention_on_the_packed_projection_itself():
+    """Q, K and V as views of one token-major tensor, O token-major too."""
+    g = gen(20)
+    H, S, D = 5, 700, 72
+    x = randn(g, S, 3, H, D, dtype=BF)
+    q, k, v = (x[:, i].transpose(0, 1) for i in range(3))
+    idx, count = lists_for(g, H, S, S, 64, 7, RAGGED(7))
+    O, L, st = attend(q, k, v, idx, count, 64, o=torch.zeros(S, H, D, dtype=BF, device="cuda").transpose(0, 1))
+    O2, L2, _ = attend(q.contiguous(), k.contiguous(), v.contiguous(), idx, count, 64)
+    assert st == 0 and torch.equal(O, O2) and torch.equal(L, L2)
+    check_attention(q, k, v, idx, count, 64, O, L)
+
+
+@pytest.mark.parametrize("H,Sq,cap", [(300, 1, 3), (3, 6400, 2), (16, 1280, 5)])
+def test_attention_many_short_lists(H, Sq, cap):
+    """Items of no, one or two tiles: the scheduler, not the tiles, sets the pace."""
+    g = gen(24)
+    q, k, v = randn(g, H, Sq, 64, dtype=BF), randn(g, 1, 500, 64, dtype=BF), randn(g, 1, 500, 64, dtype=BF)
+    for counts in (RAGGED(cap), 0, 1):
+        idx, count = lists_for(g, H, Sq, 500, 64, cap, counts)
+        O, L, st = attend(q, k, v, idx, count, 64)
+        assert st == 0
+        check_attention(q, k, v, idx, count, 64, O, L)
+
+
+def test_attention_first_call_inside_a_capture():
+    """A process whose first call of the kernel is captured: its one-time set-up is legal there."""
+    code = (
+        "import torch, partitioned_attention_state_b200 as dt\n"
+        "q = torch.randn(2, 300, 64, device='cuda').half(); k = torch.randn(2, 256, 64, device='cuda').half()\n"
+        "idx = torch.arange(4, device='cuda', dtype=torch.int32).expand(2, 3, 4).contiguous()\n"
+        "O, L = torch.zeros_like(q), torch.zeros(2, 300, device='cuda')\n"
+        "st = torch.zeros(4, dtype=torch.int32, device='cuda'); p = dt.sparse_params(q, k, k, O, 64, 4)\n"
+        "qm, km = torch.zeros(2, 3, 64, device='cuda'), torch.zeros(2, 4, 64, device='cuda')\n"
+        "n, m = dt.norm_rope_params(q, norm=False), dt.norm_rope_params(k=k, norm=False)\n"
+        "s = dt.select_params(2, 2, 3, 4, 64, 4); c = torch.zeros(2, 3, dtype=torch.int32, device='cuda')\n"
+        "g = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(g):\n"
+        "    dt.dt_qk_norm_rope(n, q, None, None, None, None, None, None, None, None, qm)\n"
+        "    dt.dt_qk_norm_rope(m, None, k, None, None, None, None, None, None, None, None, km)\n"
+        "    dt.dt_block_select(s, qm, km, idx, c)\n"
+        "    dt.dt_attn_block_sparse(p, q, k, k, idx, c, O, L, st)\n"
+        "g.replay(); torch.cuda.synchronize()\n"
+        "ref = torch.softmax(q.float() @ k.float().transpose(1, 2) / 8, -1) @ k.float()\n"
+        "assert int(st[0]) == 0 and float((O.float() - ref).abs().max()) < 0.01\n")
+    res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stderr[-2000:]
 
 
 @pytest.mark.parametrize("block", [64, 128])
@@ -604,3 +694,34 @@ def test_session_sparse_step_captured_in_a_graph():
     sess2.set_projection(qkv)
     sess2.step_sparse(6, remeasure=False)
     assert torch.equal(sess.O, sess2.O) and torch.equal(sess.lists[0], sess2.lists[0])
+
+
+def test_session_sparse_steps_of_several_sizes_beside_a_captured_one():
+    """Other topk and k_block in between leave a captured sparse step's buffers alone."""
+    g = gen(67)
+    H, S, D = 3, 900, 64
+    qkv = randn(g, S, 3 * H * D, dtype=BF)
+    sess = Session(H, S, D, P=2, cache=False)
+    sess.set_projection(qkv)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sess.step_sparse(5)
+    graph.replay()
+    torch.cuda.synchronize()
+    want_o, want_l = sess.O.clone(), sess.lists[0].clone()
+    lists = sess.lists
+    sess.step_sparse(3, k_block=128)
+    with pytest.raises(ValueError):
+        sess.step_sparse(3, remeasure=False)          # the means at hand are of 128-row blocks
+    sess.step_sparse(4, remeasure=False, k_block=128)
+    sess.set_inputs(sess.Q.clone(), sess.K.clone(), sess.V.clone())
+    with pytest.raises(ValueError):
+        sess.step_sparse(4, remeasure=False, k_block=128)
+    with pytest.raises(ValueError):
+        sess.step_sparse(4, k_block=96)
+    with pytest.raises(ValueError):
+        sess.set_projection(qkv[:, :-8])
+    sess.O.zero_()
+    graph.replay()
+    sess.check()
+    assert torch.equal(sess.O, want_o) and torch.equal(lists[0], want_l)
