@@ -382,17 +382,19 @@ int norm_rope_dispatch(const NormRopeArgs& a, unsigned grid, cudaStream_t st) {
 //
 // Scores on the 64-bit tensor cores (m8n8k4): fp32 operands widen exactly, a
 // product of two is exact, and only the sum rounds, at 2^-53.  A warp owns 16
-// key blocks at a time and R (8 or 16, padded with zero rows) query blocks; the
+// key blocks at a time and the CTA's R query blocks (padded to 8 with zero rows); the
 // queries lie in shared memory as doubles, the keys come from L2 straight into
 // the fragments.  The order of a dot product's terms is free, so lane j of a
 // quad takes the consecutive columns 4j .. 4j+3 of each 16 for its 4 k-steps:
 // 16-byte loads on both sides instead of one element per step.
 //
-// Then a warp per row finds the topk-th largest by a radix selection, 8 bits a
-// pass from the highest bit in which the row's keys differ (order-preserving
-// 64-bit keys), ending as soon as a digit's keys are all wanted, and writes the
-// chosen blocks in increasing order by ballots.
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+// Then a warp per row finds the topk-th score and writes the chosen blocks in
+// increasing order by ballots.  It bins the scores evenly over the row's range and
+// ranks the few in the bin that holds the topk-th: digits of the scores' bit
+// patterns, which a radix selection bins by, need three passes over the row and put
+// most of it into two or three counters in the first (96 us in all on the case
+// below, 75 this way; the scores alone are 37 us of the 64-bit pipe).
+constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 
 // order-preserving key of a score; NaN counts as -infinity
 __device__ __forceinline__ uint64_t order_key(double x) {
@@ -401,6 +403,34 @@ __device__ __forceinline__ uint64_t order_key(double x) {
   const int64_t b = __double_as_longlong(x);
   return (uint64_t)(b < 0 ? ~b : (b | (int64_t)0x8000000000000000ull));
 }
+// the score of an order key
+__device__ __forceinline__ double key_score(uint64_t k) {
+  return __longlong_as_double((k >> 63) ? (int64_t)(k & 0x7fffffffffffffffull) : (int64_t)~k);
+}
+// The bin, counted from the highest, in which the running count of a warp's 256-bin histogram reaches `want` (>= 1, at
+// most the total); want becomes the rank inside it, size its count.  Lane l sums bins 255-8l .. 248-8l.
+__device__ __forceinline__ int find_bin(const uint32_t* hs, int lane, int& want, uint32_t& size) {
+  uint32_t c[8], mine = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) mine += c[e] = hs[255 - 8 * lane - e];
+  uint32_t run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t u = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += u;
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, run >= (uint32_t)want)) - 1;
+  uint32_t before = run - mine, n = 0;
+  int bin = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (n == 0 && before + c[e] >= (uint32_t)want) { bin = 255 - 8 * lane - e; n = c[e]; }
+    else if (n == 0) before += c[e];
+  }
+  size = __shfl_sync(0xffffffffu, n, src);
+  want -= (int)__shfl_sync(0xffffffffu, before, src);
+  return __shfl_sync(0xffffffffu, bin, src);
+}
 __device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
   asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
                : "+d"(c[0]), "+d"(c[1]) : "d"(a), "d"(b));
@@ -408,15 +438,17 @@ __device__ __forceinline__ void mma_f64(double (&c)[2], double a, double b) {
 
 __host__ __device__ inline int select_ldq(int D) { return (D + 15) / 16 * 16 + 2; }   // doubles; +2 spreads the banks
 
-template <int MT>                                   // 8-row tiles of query blocks: R <= 8 * MT
-__global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_select_params p, const float* q_mean,
+constexpr int kSelRows = 8;                         // query blocks of a CTA at most: one MMA row tile
+
+__global__ void __launch_bounds__(kSelThreads, 4) block_select_kernel(const dt_select_params p, const float* q_mean,
                                                                       const float* k_mean, int32_t* idx,
                                                                       int32_t* count, int qtiles, int R) {
   extern __shared__ double sm[];
   __shared__ uint32_t hist[kSelWarps][256];
   const int D = p.D, nk = p.nk, ldq = select_ldq(D);
-  double* sQ = sm;                                  // [8 * MT][ldq], zeros past the rows and columns
-  uint64_t* keys = reinterpret_cast<uint64_t*>(sQ + 8 * MT * ldq);       // [R][nk]
+  double* sQ = sm;                                  // [kSelRows][ldq], zeros past the rows and columns
+  uint64_t* keys = reinterpret_cast<uint64_t*>(sQ + kSelRows * ldq);     // [R][nk]
+  uint8_t* bins = reinterpret_cast<uint8_t*>(keys + (int64_t)R * nk);    // [R][nk], see below
   const int h = blockIdx.x / qtiles, q0 = (blockIdx.x - h * qtiles) * R;
   const int rows = min(R, p.nq - q0);
   const float* km = k_mean + (int64_t)(h / (p.H / p.Hkv)) * nk * D;
@@ -425,13 +457,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_s
   const int g = lane >> 2, j = lane & 3;            // a fragment's row (query or key) and quad lane
   const double scale = 1.0 / sqrt((double)D);
 
-  for (int i = tid; i < 8 * MT * ldq; i += kSelThreads) {
+  for (int i = tid; i < kSelRows * ldq; i += kSelThreads) {
     const int r = i / ldq, c = i - r * ldq;
     sQ[i] = r < rows && c < D ? (double)qm[(int64_t)r * D + c] : 0.0;
   }
   __syncthreads();
   for (int n0 = 16 * warp; n0 < nk; n0 += 16 * kSelWarps) {
-    double acc[MT][2][2] = {};
+    double acc[2][2] = {};
     const float* kr[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) kr[n] = km + (int64_t)min(n0 + 8 * n + g, nk - 1) * D;
@@ -441,146 +473,196 @@ __global__ void __launch_bounds__(kSelThreads, 2) block_select_kernel(const dt_s
       float4 kb[2];
 #pragma unroll
       for (int n = 0; n < 2; ++n) kb[n] = k0 < D ? __ldg(reinterpret_cast<const float4*>(kr[n] + k0)) : zero;
-      double qa[MT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const double2* src = reinterpret_cast<const double2*>(sQ + (8 * m + g) * ldq + k0);
-        const double2 u = src[0], v = src[1];
-        qa[m][0] = u.x; qa[m][1] = u.y; qa[m][2] = v.x; qa[m][3] = v.y;
-      }
+      const double2* src = reinterpret_cast<const double2*>(sQ + g * ldq + k0);
+      const double2 u = src[0], v = src[1];
+      const double qa[4] = {u.x, u.y, v.x, v.y};
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const double b = t == 0 ? kb[n].x : (t == 1 ? kb[n].y : (t == 2 ? kb[n].z : kb[n].w));
-#pragma unroll
-          for (int m = 0; m < MT; ++m) mma_f64(acc[m][n], qa[m][t], b);
-        }
+        for (int n = 0; n < 2; ++n)
+          mma_f64(acc[n], qa[t], t == 0 ? kb[n].x : (t == 1 ? kb[n].y : (t == 2 ? kb[n].z : kb[n].w)));
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * m + g, c = n0 + 8 * n + 2 * j + e;
-          if (r < rows && c < nk) keys[(int64_t)r * nk + c] = order_key(acc[m][n][e] * scale);
-        }
+      for (int e = 0; e < 2; ++e) {
+        const int c = n0 + 8 * n + 2 * j + e;
+        if (g < rows && c < nk) keys[(int64_t)g * nk + c] = order_key(acc[n][e] * scale);
+      }
   }
   __syncthreads();
 
   const int topk = min(p.topk, nk), lo_keep = p.keep_first, hi_keep = nk - p.keep_last;
+  const uint32_t below = (1u << lane) - 1u;
   for (int r = warp; r < rows; r += kSelWarps) {
     uint64_t* kr = keys + (int64_t)r * nk;
     uint32_t* hs = hist[warp];
     // Keys kept by position get the highest key; under a margin, keys below the floor the lowest (0, which no
-    // score has), and are never chosen.  same: the bits in which all keys agree.
+    // score has), and are never chosen.
     const uint64_t forced = ~0ull;
-    uint64_t floor_key = 0;
-    if (p.margin < INFINITY && nk > 0) {
-      uint64_t best = 0;
-#pragma unroll 4
-      for (int i = lane; i < nk; i += 32) best = max(best, kr[i]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) best = max(best, (uint64_t)__shfl_xor_sync(0xffffffffu, best, o));
-      const int64_t b = (best >> 63) ? (int64_t)(best & 0x7fffffffffffffffull) : (int64_t)~best;
-      floor_key = order_key(__longlong_as_double(b) - p.margin);
-    }
-    uint64_t all_and = ~0ull, all_or = 0;
+    uint64_t kmax = 0, kmin = ~0ull;
 #pragma unroll 4
     for (int i = lane; i < nk; i += 32) {
-      uint64_t k = kr[i];
-      if (i < lo_keep || i >= hi_keep) kr[i] = k = forced;
-      else if (k < floor_key) kr[i] = k = 0;
-      all_and &= k;
-      all_or |= k;
+      kmax = max(kmax, kr[i]);
+      kmin = min(kmin, kr[i]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      all_and &= __shfl_xor_sync(0xffffffffu, all_and, o);
-      all_or |= __shfl_xor_sync(0xffffffffu, all_or, o);
+      kmax = max(kmax, (uint64_t)__shfl_xor_sync(0xffffffffu, kmax, o));
+      kmin = min(kmin, (uint64_t)__shfl_xor_sync(0xffffffffu, kmin, o));
     }
+    const uint64_t floor_key = p.margin < INFINITY && nk > 0 ? order_key(key_score(kmax) - p.margin) : 0;
+    // The last key to be taken: (kt, it), the topk-th in the order of scores (highest first) and indices.  First by
+    // bins 1 .. 254 over the row's range (0: below the floor, 255: kept by position): a bin is a monotone function of
+    // the score (conversion, difference, product and truncation all are), so the bins above the topk-th key's are
+    // taken whole, and its own usually holds a few keys.
+    const float fmin = (float)key_score(kmin), per = 253.f / ((float)key_score(kmax) - fmin);
+    const bool binned = topk > 0 && per < INFINITY && per > 0.f;   // finite and not all equal
+    uint8_t* br = bins + (int64_t)r * nk;
+    int want = topk;                                // 1-based rank of that key among those still in question
+    for (int i = lane; i < 256; i += 32) hs[i] = 0;
     __syncwarp();
-    // the topk-th largest key: `prefix` holds the bits found, `want` the 1-based rank among the keys that match it
-    const uint64_t differ = all_and ^ all_or;
-    int shift = differ ? 64 - __clzll(differ) : 0;   // bits below `shift` are still open
-    uint64_t prefix = shift == 64 ? 0ull : all_and >> shift << shift;
-    int want = topk;
-    while (shift > 0 && topk > 0) {
-      const int bits = min(8, shift);
-      const uint64_t hi = shift == 64 ? 0ull : ~0ull << shift;
-      shift -= bits;
-      for (int i = lane; i < 256; i += 32) hs[i] = 0;
-      __syncwarp();
+    int held = 0, live = 0;                         // keys kept by position, and other keys above the floor
 #pragma unroll 4
-      for (int i = lane; i < nk; i += 32) {
-        const uint64_t k = kr[i];
-        if ((k & hi) == prefix) atomicAdd(&hs[(uint32_t)(k >> shift) & ((1u << bits) - 1u)], 1u);
+    for (int i = lane; i < nk; i += 32) {
+      const uint64_t k = kr[i];
+      int b = 0;
+      if (i < lo_keep || i >= hi_keep) {
+        kr[i] = forced;
+        b = 255;
+        ++held;
+      } else if (k < floor_key) {
+        kr[i] = 0;
+      } else {
+        ++live;
+        if (binned) {
+          b = 1 + min(253, (int)(((float)key_score(k) - fmin) * per));
+          atomicAdd(&hs[b], 1u);
+        }
       }
-      __syncwarp();
-      // lane l holds bins 255-8l .. 248-8l; the bin in which the running count reaches `want`
-      uint32_t c[8], mine = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mine += c[e] = hs[255 - 8 * lane - e];
-      uint32_t run = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += u;
-      }
-      const int src = __ffs(__ballot_sync(0xffffffffu, run >= (uint32_t)want)) - 1;
-      uint32_t before = run - mine, size = 0;
-      int bin = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (size == 0 && before + c[e] >= (uint32_t)want) { bin = 255 - 8 * lane - e; size = c[e]; }
-        else if (size == 0) before += c[e];
-      }
-      bin = __shfl_sync(0xffffffffu, bin, src);
-      want -= (int)__shfl_sync(0xffffffffu, before, src);
-      size = __shfl_sync(0xffffffffu, size, src);
-      prefix |= (uint64_t)bin << shift;
-      __syncwarp();
-      if (size == (uint32_t)want) break;             // every key with this prefix is wanted: no need to tell them apart
+      br[i] = (uint8_t)b;
     }
-    // chosen: the prefix and above; where keys equal to it are left over (shift 0), the first `want` of those
+    held = __reduce_add_sync(0xffffffffu, held);
+    live = __reduce_add_sync(0xffffffffu, live);
+    __syncwarp();
+    want -= held;
+    uint64_t kt = 0;
+    int it = nk, tb = 0;                            // tb > 0: only the keys of bin tb need comparing
+    bool done = false;
+    if (topk == 0 || live <= want) {
+      kt = 1;                                       // everything above the floor
+      done = true;
+    } else if (want <= 0) {
+      kt = forced;                                  // the kept ones alone
+      done = true;
+    } else if (binned) {
+      uint32_t size;
+      tb = find_bin(hs, lane, want, size);
+      done = size <= 32;
+      if (done) {
+        // the bin's keys, in order of index, one per lane (the histogram is done with)
+        __syncwarp();
+        int n = 0;
+        for (int i0 = 0; i0 < nk; i0 += 32) {
+          const bool in = i0 + lane < nk && br[i0 + lane] == tb;
+          const uint32_t m = __ballot_sync(0xffffffffu, in);
+          if (in) hs[n + __popc(m & below)] = i0 + lane;
+          n += __popc(m);
+        }
+        __syncwarp();
+        const int at = lane < n ? (int)hs[lane] : 0;
+        const uint64_t mine = lane < n ? kr[at] : 0;
+        int rank = 1;                               // place among them
+        for (int o = 0; o < n; ++o) {
+          const uint64_t v = __shfl_sync(0xffffffffu, mine, o);
+          rank += v > mine || (v == mine && o < lane);
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, lane < n && rank == want)) - 1;
+        kt = __shfl_sync(0xffffffffu, mine, src);
+        it = __shfl_sync(0xffffffffu, at, src);
+      } else {
+        tb = 0;
+      }
+    }
+    if (!done) {
+      // Many equal or nearly equal keys, or infinities: 8 bits of the key a pass from the highest bit in which the
+      // row's keys differ, ending as soon as all keys of a digit are wanted.  Where keys equal to the last are left
+      // over, the lowest indices take them.
+      uint64_t all_and = ~0ull, all_or = 0;
+      for (int i = lane; i < nk; i += 32) {
+        all_and &= kr[i];
+        all_or |= kr[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        all_and &= __shfl_xor_sync(0xffffffffu, all_and, o);
+        all_or |= __shfl_xor_sync(0xffffffffu, all_or, o);
+      }
+      want = topk;                                  // the kept keys count here: they are the highest
+      const uint64_t differ = all_and ^ all_or;
+      int shift = differ ? 64 - __clzll(differ) : 0;        // bits below `shift` are still open
+      uint64_t prefix = shift == 64 ? 0ull : all_and >> shift << shift;
+      uint32_t size = nk;
+      while (shift > 0 && size != (uint32_t)want) {
+        const int bits = min(8, shift);
+        const uint64_t hi = shift == 64 ? 0ull : ~0ull << shift;
+        shift -= bits;
+        __syncwarp();
+        for (int i = lane; i < 256; i += 32) hs[i] = 0;
+        __syncwarp();
+        for (int i = lane; i < nk; i += 32) {
+          const uint64_t k = kr[i];
+          if ((k & hi) == prefix) atomicAdd(&hs[(uint32_t)(k >> shift) & ((1u << bits) - 1u)], 1u);
+        }
+        __syncwarp();
+        prefix |= (uint64_t)find_bin(hs, lane, want, size) << shift;
+      }
+      kt = prefix;                                  // with bits open, every key above it is wanted too
+      if (shift == 0) {
+        int left = want;                            // of the keys equal to kt
+        for (int i0 = 0; i0 < nk && left > 0; i0 += 32) {
+          const uint32_t m = __ballot_sync(0xffffffffu, i0 + lane < nk && kr[i0 + lane] == kt);
+          if (__popc(m) >= left) it = i0 + (int)__fns(m, 0, left);
+          left -= __popc(m);
+        }
+      }
+    }
     int32_t* out = idx + ((int64_t)h * p.nq + q0 + r) * p.topk;
-    const uint64_t open = shift == 64 ? 0ull : ~0ull << shift;
-    int n = 0, eq = 0;
+    int n = 0;
+    if (tb > 0) {
+#pragma unroll 4
+      for (int i0 = 0; i0 < nk; i0 += 32) {
+        const int i = i0 + lane, b = i < nk ? br[i] : 0;
+        bool take = b > tb;
+        if (b == tb) {
+          const uint64_t k = kr[i];
+          take = k > kt || (k == kt && i <= it);
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, take);
+        if (take) out[n + __popc(m & below)] = i;
+        n += __popc(m);
+      }
+    } else {
 #pragma unroll 2
-    for (int i0 = 0; i0 < nk && topk > 0; i0 += 32) {
-      const int i = i0 + lane;
-      const uint64_t k = i < nk ? kr[i] : 0, kp = k & open;
-      const bool same = i < nk && kp == prefix;
-      const uint32_t below = (1u << lane) - 1u;
-      const uint32_t em = __ballot_sync(0xffffffffu, same);
-      const bool take = i < nk && k != 0 && (kp > prefix || (same && eq + __popc(em & below) < want));
-      const uint32_t tm = __ballot_sync(0xffffffffu, take);
-      if (take) out[n + __popc(tm & below)] = i;
-      n += __popc(tm);
-      eq += __popc(em);
+      for (int i0 = 0; i0 < nk; i0 += 32) {
+        const int i = i0 + lane;
+        const uint64_t k = i < nk && topk > 0 ? kr[i] : 0;
+        const bool take = k != 0 && (k > kt || (k == kt && i <= it));
+        const uint32_t m = __ballot_sync(0xffffffffu, take);
+        if (take) out[n + __popc(m & below)] = i;
+        n += __popc(m);
+      }
     }
     for (int i = n + lane; i < p.topk; i += 32) out[i] = -1;
     if (lane == 0) count[(int64_t)h * p.nq + q0 + r] = n;
+    __syncwarp();                                   // the histogram is cleared for the next row
   }
 }
 
-constexpr int kSelSmemMax = 160 * 1024;            // one row of DT_SELECT_MAX_BLOCKS keys and 8 of queries at D = 128
+constexpr int kSelSmemMax = 160 * 1024;            // one row of DT_SELECT_MAX_BLOCKS keys and bins, queries of D = 128
 
 size_t select_smem(int R, int D, int nk) {
-  return ((size_t)(R > 8 ? 16 : 8) * select_ldq(D) + (size_t)R * nk) * 8;
-}
-
-template <int MT>
-int select_launch(const dt_select_params& p, const float* qm, const float* km, int32_t* idx, int32_t* count, int R,
-                  cudaStream_t st) {
-  const size_t smem = select_smem(R, p.D, p.nk);
-  // the most that any call asks for, so that calls of other sizes never lower it under a call in flight
-  static std::atomic<int> allowed[64];
-  if (!allow_smem(block_select_kernel<MT>, allowed, kSelSmemMax)) return DT_ERR_CUDA;
-  const int qtiles = cdiv(p.nq, R);
-  block_select_kernel<MT><<<(unsigned)(p.H * qtiles), kSelThreads, smem, st>>>(p, qm, km, idx, count, qtiles, R);
-  return launched();
+  return (size_t)kSelRows * select_ldq(D) * 8 + (size_t)R * nk * 9;
 }
 
 }  // namespace
@@ -612,13 +694,18 @@ int launch_qk_norm_rope(NormRopeArgs a, int sms, cudaStream_t stream) {
 
 int launch_block_select(const dt_select_params& p, const float* q_mean, const float* k_mean, int32_t* idx,
                         int32_t* count, cudaStream_t stream) {
-  // Query blocks per CTA: as many as there are, up to 16, while the keys of
-  // the rows leave room for a second CTA on the SM (one scores while the other
-  // selects); long rows take what one CTA may have.
-  int R = 16;
-  while (R > 1 && (R / 2 >= p.nq || select_smem(R, p.D, p.nk) > 100 * 1024)) R /= 2;
-  return R > 8 ? select_launch<2>(p, q_mean, k_mean, idx, count, R, stream)
-               : select_launch<1>(p, q_mean, k_mean, idx, count, R, stream);
+  // Query blocks per CTA: as many as there are, up to 8, while the keys of the rows leave room for four CTAs on an SM
+  // (some score while others select: 75 us on 40 heads of 256 x 512 blocks at D = 128, against 79 with 16 rows and
+  // two CTAs); longer rows take what they need.
+  int R = kSelRows;
+  while (R > 1 && (R / 2 >= p.nq || select_smem(R, p.D, p.nk) > 46 * 1024)) R /= 2;
+  const size_t smem = select_smem(R, p.D, p.nk);
+  // the most that any call asks for, so that calls of other sizes never lower it under a call in flight
+  static std::atomic<int> allowed[64];
+  if (!allow_smem(block_select_kernel, allowed, kSelSmemMax)) return DT_ERR_CUDA;
+  const int qtiles = cdiv(p.nq, R);
+  block_select_kernel<<<(unsigned)(p.H * qtiles), kSelThreads, smem, stream>>>(p, q_mean, k_mean, idx, count, qtiles, R);
+  return launched();
 }
 
 }  // namespace dt
