@@ -251,6 +251,39 @@ def test_select_largest_row():
     assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
 
 
+@pytest.mark.parametrize("kind", ["outlier", "clusters", "steps", "ulps", "huge", "tiny"])
+@pytest.mark.parametrize("nk", [40, 300, 1000])
+def test_select_uneven_scores(kind, nk):
+    """Scores that crowd into one bin of the row's range, in every way the selection tells them apart."""
+    g = gen(nk)
+    qm = torch.zeros(2, 5, 64, device="cuda")
+    qm[..., 0] = 1.0
+    km = torch.zeros(1, nk, 64, device="cuda")
+    x = torch.randn(nk, generator=g, device="cuda")
+    if kind == "outlier":                            # one score far above: the rest share a bin
+        x[nk // 2] = 1e9
+    elif kind == "clusters":
+        x = x * 1e-4 + torch.where(torch.arange(nk, device="cuda") % 3 == 0, 7.0, -2.0)
+    elif kind == "steps":                            # few values, many ties
+        x = torch.round(x * 2)
+    elif kind == "ulps":
+        x = 1.0 + torch.randint(0, 40, (nk,), generator=g, device="cuda") * 2.0 ** -23
+    elif kind == "huge":                             # the range itself overflows fp32
+        x = x * 1e38
+        qm[..., 0] = 1e30
+    else:
+        x = x * 1e-38
+        qm[..., 0] = 1e-30
+    km[0, :, 0] = x
+    for topk, first, last, margin in ((1, 0, 0, math.inf), (nk // 3, 0, 0, math.inf), (nk // 3, 3, 2, 0.25),
+                                      (nk - 1, 0, 1, math.inf), (33, 33, 0, math.inf), (20, 0, 0, 1e-6)):
+        if first + last > topk:
+            continue
+        got, ref = run_select(qm, km, topk, first, last, margin), sp.block_select(np64(qm), np64(km), topk, first, last, margin)
+        np.testing.assert_array_equal(got[0], ref[0])
+        np.testing.assert_array_equal(got[1], ref[1])
+
+
 def test_select_equal_scores_take_the_lowest_indices():
     qm = torch.ones(1, 3, 64, device="cuda")
     km = torch.zeros(1, 100, 64, device="cuda")
