@@ -198,13 +198,13 @@ __device__ __forceinline__ Item make_item(const SparseParams& p, int item, int r
   it.h = (int)((unsigned)item / (unsigned)p.nqb);
   it.q0 = (item - it.h * p.nqb) * kTile;
   it.rows = imin(kTile, p.Sq - it.q0);
+  const int32_t* list = p.idx + (int64_t)item * p.cap;
   const int count = p.count ? __ldg(p.count + item) : p.cap;
   it.n = imin(imax(count, 0), p.cap);
   const int nt = (it.n + p.per_tile - 1) / p.per_tile;
   it.t0 = (int)((int64_t)nt * rank / p.split);
   it.nt = (int)((int64_t)nt * (rank + 1) / p.split) - it.t0;
   const unsigned whole = (unsigned)p.Sk / (unsigned)(kTile / p.per_tile);     // blocks below this one are whole
-  const int32_t* list = p.idx + (int64_t)item * p.cap;
   int at = p.per_tile == 2 && (it.n & 1) ? it.n - 1 : it.n;
   bool bad = count != it.n;
   for (int j = 0; j < it.n; j += 128) {
@@ -603,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       }
       __syncwarp();
     }
+    if (p.split > 1) cluster_sync_all();
   } else if (warp < kWarpEpi) {
     regs_set<kLaunchRegs, kRegsSoftmax>();
     // ------------------------------------------------------------ softmax
@@ -733,6 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       g0 += nt;
     }
   sm_done:;
+    __syncwarp();
+    if (p.split > 1) cluster_sync_all();
   } else {
     regs_set<kLaunchRegs, kRegsEpilogue>();
     // ------------------------------------------------------------ epilogue
@@ -806,6 +809,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
             *reinterpret_cast<uint4*>(at + r * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
         }
+      } else if (p.split > 1) {
+        // (a warp without rows has nothing to hand over)
+        constexpr int kStep = DP % 32 ? 16 : 32;
+        if (r - lane < it.rows)
+#pragma unroll 1
+          for (int c0 = 0; c0 < DP; c0 += kStep) {
+            uint32_t op[kStep];
+#pragma unroll
+            for (int c = 0; c < kStep; c += 16) tmem_ld16p(oaddr + c0 + c, op + c);
+            tmem_wait_ld();
+            after_wait<kStep>(op);
+#pragma unroll
+            for (int c = 0; c < kStep; c += 4)
+              if (valid && c0 + c < D)
+                *reinterpret_cast<float4*>(part + part_chunk<DP>(r, (c0 + c) / 4)) =
+                    make_float4(u2f(op[c]), u2f(op[c + 1]), u2f(op[c + 2]), u2f(op[c + 3]));
+          }
+        tc_fence_before();
+        mbar_arrive(&bars[C::bOFree]);
       } else {
 #pragma unroll 1
         for (int c0 = 0; c0 < DP; c0 += 16) {
@@ -816,17 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
             if (c0 + c >= D) break;
             float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = u2f(op[c + e]);
-            if (p.split > 1) {
-#pragma unroll
-              for (int e = 0; e < 8; e += 4)
-                *reinterpret_cast<float4*>(part + part_chunk<DP>(r, (c0 + c + e) / 4)) =
-                    make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-            } else if (valid) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : x[e] * inv;
-              store_out8<F16>(p, orow + c0 + c, x);
-            }
+            for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : u2f(op[c + e]) * inv;
+            if (valid) store_out8<F16>(p, orow + c0 + c, x);
           }
         }
       }
@@ -848,45 +861,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
       ++nq;
     }
   ep_done:;
+    __syncwarp();
+    if (p.split > 1) {
+      // Join of the cluster's states of its one item: M = max m_i, w_i =
+      // 2^(m_i - M), O = sum w_i O_i / sum w_i l_i.  CTA `rank` joins 8-column
+      // chunks rank, rank + split, ... of the item's rows.  Four CTAs' values are
+      // loaded together: one by one their latencies were most of a short call's
+      // end.  Every warp reaches both barriers whatever its role met before.
+      cluster_sync_all();
+      if (!*abort_flag) {
+        const Item it0 = info[0];                         // the one item, untouched since
+        const uint32_t a_m = smem_u32(stat_m), a_l = smem_u32(stat_l), a_o = smem_u32(sK);
+        const int nchunk = it0.rows * (D / 8);
+        // each CTA starts at its own state, so that they do not all read one CTA's at once
+        auto peer = [&](int k) { return rank + k < p.split ? rank + k : rank + k - p.split; };
+        for (int i = r * p.split + rank; i < nchunk; i += 128 * p.split) {
+          const int row = i / (D / 8), c = 8 * (i - row * (D / 8));
+          float M = neg_inf();
+          for (int k0 = 0; k0 < p.split; k0 += 4) {
+            float m[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              m[k] = neg_inf();
+              if (k0 + k < p.split) m[k] = ld_cluster(map_rank(a_m + 4 * row, peer(k0 + k)));
+            }
+            M = fmaxf(M, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+          }
+          const float Mr = M == neg_inf() ? 0.f : M;
+          float x[8] = {}, l = 0.f;
+          for (int k0 = 0; k0 < p.split; k0 += 4) {
+            float m[4], lk[4];
+            float4 u[4], v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              lk[k] = 0.f;
+              if (k0 + k >= p.split) continue;
+              const int from = peer(k0 + k);
+              m[k] = ld_cluster(map_rank(a_m + 4 * row, from));
+              lk[k] = ld_cluster(map_rank(a_l + 4 * row, from));
+              u[k] = ld_cluster4(map_rank(a_o + 4 * part_chunk<DP>(row, c / 4), from));
+              v[k] = ld_cluster4(map_rank(a_o + 4 * part_chunk<DP>(row, c / 4 + 1), from));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (lk[k] == 0.f) continue;                 // an empty state's O was never written
+              const float w = ex2(m[k] - Mr);
+              l = fmaf(w, lk[k], l);
+              x[0] = fmaf(w, u[k].x, x[0]); x[1] = fmaf(w, u[k].y, x[1]);
+              x[2] = fmaf(w, u[k].z, x[2]); x[3] = fmaf(w, u[k].w, x[3]);
+              x[4] = fmaf(w, v[k].x, x[4]); x[5] = fmaf(w, v[k].y, x[5]);
+              x[6] = fmaf(w, v[k].z, x[6]); x[7] = fmaf(w, v[k].w, x[7]);
+            }
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] *= inv;
+          store_out8<F16>(p, it0.h * p.o_head + (int64_t)(it0.q0 + row) * p.o_row + c, x);
+          if (c == 0) p.L[(int64_t)it0.h * p.Sq + it0.q0 + row] = l == 0.f ? neg_inf() : (M + lg2(l)) * kLn2;
+        }
+      }
+      __syncwarp();
+    }
   }
 
-  if (p.split > 1) {
-    // Join of the cluster's states of its one item: M = max m_i, w_i =
-    // 2^(m_i - M), O = sum w_i O_i / sum w_i l_i.  CTA `rank` joins 8-column
-    // chunks rank, rank + split, ... of the item's rows; every thread reaches
-    // both barriers whatever its role met before.
-    __syncwarp();
-    cluster_sync_all();
-    if (warp >= kWarpEpi && warp < kWarpMma && !*abort_flag) {
-      const Item it = info[0];                            // the one item, untouched since
-      const uint32_t a_m = smem_u32(stat_m), a_l = smem_u32(stat_l), a_o = smem_u32(sK);
-      const int nchunk = it.rows * (D / 8);
-      for (int i = (threadIdx.x - kWarpEpi * 32) * p.split + rank; i < nchunk; i += 128 * p.split) {
-        const int row = i / (D / 8), c = 8 * (i - row * (D / 8));
-        float M = neg_inf();
-        for (int k = 0; k < p.split; ++k) M = fmaxf(M, ld_cluster(map_rank(a_m + 4 * row, k)));
-        const float Mr = M == neg_inf() ? 0.f : M;
-        float x[8] = {}, l = 0.f;
-        for (int k = 0; k < p.split; ++k) {
-          const float lk = ld_cluster(map_rank(a_l + 4 * row, k));
-          if (lk == 0.f) continue;                        // an empty state, and its O was never written
-          const float w = ex2(ld_cluster(map_rank(a_m + 4 * row, k)) - Mr);
-          const float4 u = ld_cluster4(map_rank(a_o + 4 * part_chunk<DP>(row, c / 4), k));
-          const float4 v = ld_cluster4(map_rank(a_o + 4 * part_chunk<DP>(row, c / 4 + 1), k));
-          l = fmaf(w, lk, l);
-          x[0] = fmaf(w, u.x, x[0]); x[1] = fmaf(w, u.y, x[1]); x[2] = fmaf(w, u.z, x[2]); x[3] = fmaf(w, u.w, x[3]);
-          x[4] = fmaf(w, v.x, x[4]); x[5] = fmaf(w, v.y, x[5]); x[6] = fmaf(w, v.z, x[6]); x[7] = fmaf(w, v.w, x[7]);
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= inv;
-        store_out8<F16>(p, it.h * p.o_head + (int64_t)(it.q0 + row) * p.o_row + c, x);
-        if (c == 0) p.L[(int64_t)it.h * p.Sq + it.q0 + row] = l == 0.f ? neg_inf() : (M + lg2(l)) * kLn2;
-      }
-    }
-    __syncwarp();
-    cluster_sync_all();                                   // no CTA leaves while another reads its state
-  }
+  if (p.split > 1) cluster_sync_all();                    // no CTA leaves while another reads its state
   tc_fence_before();
   __syncthreads();
   if (warp == kWarpMma) {
