@@ -28,13 +28,17 @@ int cdiv(int a, int b) { return (a + b - 1) / b; }
 // cos and sin of 2 pi t, t = pos * turns, where only t's fraction counts: with
 // turns as a 64-bit binary fraction T, pos * T mod 2^64 is that fraction
 // without any reduction, off by at most |pos| 2^-65 turns, and needs no 64-bit
-// floating point.  Its upper 32 bits, signed, are split into a float and the
-// remainder: sincospif of the float, then the angle-sum formula to first order
-// for the remainder (at most 2^-25 turns, so the second-order term is below
-// 2^-45): full fp32 accuracy.  A CTA owns kRopeTokens tokens, a thread two pairs of
-// a token (16 bytes of the table) at a time; T and the axes lie in shared
-// memory, since lanes with different pairs would serialise on the parameter bank.
+// floating point.  Its upper 32 bits split into the nearest quarter turn and a
+// rest |x| <= 1/8 turn, on which sin(2 pi x) / x and cos(2 pi x) are
+// polynomials in x^2 (minimax by Remez exchange: 1.3e-9 and 5e-11), two pairs in
+// each packed operation.  With the rounding of x the results are within 2^-23.
+// A CTA owns kRopeTokens tokens, a thread two pairs of a token (16 bytes of the
+// table) at a time; T and the axes lie in shared memory, since lanes with
+// different pairs would serialise on the parameter bank.  The library's sincospif and
+// a division per element took 10.2 us for 32,760 tokens of 64 pairs.
 constexpr int kRopeThreads = 256, kRopeTokens = 32;
+
+__device__ __forceinline__ uint64_t both(float x) { return pk2(x, x); }
 
 __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const __grid_constant__ RopeTableArgs a) {
   __shared__ uint64_t turns[kMaxPairs];
@@ -45,21 +49,38 @@ __global__ void __launch_bounds__(kRopeThreads) rope_table_kernel(const __grid_c
   }
   __syncthreads();
   const int halfp = (a.pairs + 1) / 2;
+  const uint32_t inv = 0xffffffffu / halfp + 1u;    // i / halfp = i * inv >> 32 for i < 2^12, halfp <= 64 (0: halfp = 1)
   const int s0 = blockIdx.x * kRopeTokens, n = min(kRopeTokens, a.S - s0) * halfp;
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kRopeThreads) {
-    const int ds = i / halfp, p0 = 2 * (i - ds * halfp), s = s0 + ds;
-    float out[4];
+    const int ds = halfp > 1 ? (int)__umulhi(i, inv) : i, p0 = 2 * (i - ds * halfp), s = s0 + ds;
+    uint32_t q[2];
+    float x[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int pr = min(p0 + e, a.pairs - 1);
       const int64_t pos = __ldg(a.pos + (int64_t)axis[pr] * a.S + s);
-      const int u = (int)(((uint64_t)pos * turns[pr]) >> 32);           // 2^-32 turns, [-1/2, 1/2)
-      const float hi = (float)u, lo = (float)(u - (int)hi);
-      float sn, cs;
-      sincospif(hi * 0x1p-31f, &sn, &cs);
-      const float d = lo * 1.46291807926715968e-9f;                     // 2 pi 2^-32
-      out[2 * e] = fmaf(-d, sn, cs);
-      out[2 * e + 1] = fmaf(d, cs, sn);
+      const uint32_t u = (uint32_t)(((uint64_t)pos * turns[pr]) >> 32);       // 2^-32 turns
+      q[e] = (u + 0x20000000u) >> 30;
+      x[e] = (float)(int)(u - (q[e] << 30)) * 0x1p-32f;
+    }
+    const uint64_t x2 = pk2(x[0], x[1]), z = mul2(x2, x2);
+    uint64_t sp = fma2(both(-0x1.2cf8aap+6f), z, both(0x1.465a52p+6f));
+    sp = fma2(sp, z, both(-0x1.4abba8p+5f));
+    sp = mul2(fma2(sp, z, both(0x1.921fb4p+2f)), x2);
+    uint64_t cp = fma2(both(0x1.d9c364p+5f), z, both(-0x1.55c57cp+6f));
+    cp = fma2(cp, z, both(0x1.03c1dcp+6f));
+    cp = fma2(cp, z, both(-0x1.3bd3ccp+4f));
+    cp = fma2(cp, z, both(1.f));
+    float sn[2], cs[2], out[4];
+    upk2(sp, sn[0], sn[1]);
+    upk2(cp, cs[0], cs[1]);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // a quarter turn on: (c, s) -> (-s, c)
+      const float c = q[e] & 1 ? sn[e] : cs[e], sv = q[e] & 1 ? cs[e] : sn[e];
+      out[2 * e] = __uint_as_float(__float_as_uint(c) ^ (((q[e] + 1) & 2) << 30));
+      out[2 * e + 1] = __uint_as_float(__float_as_uint(sv) ^ ((q[e] & 2) << 30));
     }
     float* dst = a.table + ((int64_t)s * a.pairs + p0) * 2;
     if ((a.pairs & 1) == 0) {
@@ -207,6 +228,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) qk_norm_rope_kernel(const __g
   TO* out = static_cast<TO*>(kind == 0 ? a.Q : (kind == 1 ? a.K : a.V));
   const bool on = 8 * lane < p.D && hh < p.H + 2 * p.Hkv && in;
   int left = on ? min(p.S - s0, run) : 0;           // rows from this lane's next to the end of the run
+  const int steps = min(run, max(0, p.S - s0));     // tokens of this warp's run
   const bool store = on && out != nullptr;
   const dt_strides si = kind == 0 ? p.q_in : (kind == 1 ? p.k_in : p.v_in);
   const dt_strides so = kind == 0 ? p.q_out : (kind == 1 ? p.k_out : p.v_out);
@@ -246,7 +268,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) qk_norm_rope_kernel(const __g
   if (__all_sync(0xffffffffu, kind == 2)) {
     // values: layout and type alone
 #pragma unroll 1
-    for (int t = 0; t < run; t += kDepth)
+    for (int t = 0; t < steps; t += kDepth)
 #pragma unroll
       for (int i = 0; i < kDepth; ++i) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
@@ -263,7 +285,7 @@ __global__ void __launch_bounds__(kNormThreads, 3) qk_norm_rope_kernel(const __g
     for (int t0 = 0; t0 < run; t0 += seg) {
       uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1
-      for (int t = 0; t < seg; t += kDepth)
+      for (int t = t0; t < t0 + seg && t < steps; t += kDepth)
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) {
           asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
