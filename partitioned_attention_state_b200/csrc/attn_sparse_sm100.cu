@@ -11,14 +11,14 @@
 // -infinity; the second half of an odd list's last tile is left out of P V
 // altogether, since shared memory there holds earlier keys.
 //
-// A work item is (head, query block), and the grid has a CTA per item.  With at
-// least as many items as SMs, a running CTA takes further items over from CTAs
+// A work item is (head, query block), and the grid has a CTA per item.  With
+// more items than SMs, a running CTA takes further items over from CTAs
 // that have not started (cluster launch control), a few tiles ahead of its need: the
 // lists may have any lengths, and this balances them without a counter in
 // memory, keeps the items head-major, so that CTAs that run together read one
 // head's K and V through L2, and overlaps one item's end with the next one's
-// start.  With fewer, the `split` CTAs of a cluster take an equal run of the
-// list's tiles each and join their states (m, l, unnormalised O) through
+// start.  With at most half as many, the `split` CTAs of a cluster take an equal
+// run of the list's tiles each and join their states (m, l, unnormalised O) through
 // distributed shared memory.
 //
 // Per CTA, 16 warps (4 warpgroups, registers rebalanced with setmaxnreg):
@@ -42,9 +42,9 @@
 //               issues an MMA only every ~50 clk)
 // Tensor memory: three S/P buffers [0,384), O [384,384+DP).
 //
-// P is rounded to the 16-bit type of V for the tensor cores (relative 2^-9
-// bf16, 2^-12 fp16 per weight, averaged over a row's keys); sums, maxima and O
-// stay in fp32, and l sums the unrounded weights.
+// P is rounded to the 16-bit type of V for the tensor cores (by at most 2^-8 of
+// a weight in bf16, 2^-11 in fp16, with signs that average out over a row's keys);
+// sums, maxima and O stay in fp32, and l sums the unrounded weights.
 //
 // Every wait is bounded; one that runs out raises an abort flag shared by all
 // roles and writes DT_ERR_TIMEOUT to *status, and every role drains its
@@ -102,8 +102,23 @@ struct Cfg {
                        bKEmpty = bVFull + kNV, bVEmpty = bKEmpty + kNK, bSFull = bVEmpty + kNV,
                        bPFull = bSFull + kNS, bPVDone = bPFull + kNS, bOFull = bPVDone + kNS, bOFree = bOFull + 1,
                        bStFull = bOFree + 1, bStFree = bStFull + 1, bTok = bStFree + 1, bInfoFull = bTok + 8,
-                       bInfoFree = bInfoFull + 2, bNeed = bInfoFree + 2, bClc = bNeed + 1, bDrain = bClc + 1, bDrainPV = bDrain + 1,
+                       bInfoFree = bInfoFull + 2, bNeed = bInfoFree + 2, bClc = bNeed + 1, bDrain = bClc + 1,
+                       bDrainPV = bDrain + 1,
                        kNumBars = bDrainPV + 1 + (bDrainPV & 1 ? 0 : 1);      // even: what follows is 16-byte aligned
+  // Arrivals that complete a phase.  Where a role of whole warps arrives, each of its threads does (no single-lane
+  // branches); the rest are tensor-core commits and TMA's expected bytes.
+  static __device__ __forceinline__ int arrivals(int i) {
+    if (i >= bPFull && i < bPFull + kNS) return 4 * 32;            // a softmax set
+    if (i >= bTok && i < bTok + 8) return 32;                      // a warp of it
+    if (i == bStFull) return 8 * 32;
+    if (i == bStFree || i == bOFree) return 4 * 32;                // the epilogue
+    // a Q buffer is free when its last Q K^T is done and the 4 epilogue warps have stored O from it
+    if (i >= bQEmpty && i < bQEmpty + kNQ) return 1 + 4;
+    if (i == bNeed) return 32;                                     // the TMA warp
+    // readers of an item: TMA and two MMA warps, softmax, epilogue
+    if (i >= bInfoFree && i < bInfoFree + 2) return 3 * 32 + 8 * 32 + 4 * 32;
+    return 1;
+  }
   // per row: reference maximum, and each set's (maximum, sum) of the item
   static constexpr int kStatsBytes = 5 * 128 * 4;
   static constexpr int kSmem = kTileBytes * (kNQ + kNK + kNV) + kStatsBytes + kNumBars * 8 + 2 * 48 + 16 + 16;
@@ -333,18 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
   const int rank = p.split > 1 ? (int)cluster_rank() : 0;
 
   if (warp == kWarpTma && lane == 0) {
-    for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bars[i], 1);
-    // every thread of the arriving role arrives (no single-lane branches)
-    for (int i = 0; i < C::kNS; ++i) mbar_init(&bars[C::bPFull + i], 4 * 32);
-    for (int i = 0; i < 8; ++i) mbar_init(&bars[C::bTok + i], 32);
-    mbar_init(&bars[C::bStFull], 8 * 32);
-    mbar_init(&bars[C::bStFree], 4 * 32);
-    // a Q buffer is free when its last Q K^T is done and the 4 epilogue warps have stored O from it
-    for (int i = 0; i < C::kNQ; ++i) mbar_init(&bars[C::bQEmpty + i], 1 + 4);
-    mbar_init(&bars[C::bOFree], 4 * 32);
-    mbar_init(&bars[C::bNeed], 32);
-    // readers of an item: TMA and two MMA warps, softmax, epilogue
-    for (int i = 0; i < 2; ++i) mbar_init(&bars[C::bInfoFree + i], 3 * 32 + 8 * 32 + 4 * 32);
+    for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bars[i], C::arrivals(i));
     *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async();
