@@ -58,7 +58,7 @@
 #include "../../include/dt.h"
 #include "attn_sparse.h"
 #include "geometry.h"
-#include "sm100.cuh"
+#include "sm100_more.cuh"
 
 namespace dt {
 namespace {

@@ -13,7 +13,7 @@
 #include <atomic>
 
 #include "../../include/dt.h"
-#include "sm100.cuh"
+#include "sm100_more.cuh"
 #include "token_ops.h"
 
 namespace dt {
