@@ -410,7 +410,8 @@ extern "C" int dt_qk_norm_rope(const dt_norm_rope_params* p, const void* q, cons
   // in place: each element is read and written by one thread only if both sides are laid out alike
   for (int i = 0; i < 3; ++i)
     if (t[i].p && t[i].p == t[i + 3].p &&
-        (p->in_type != p->out_type || t[i].s.row != t[i + 3].s.row || t[i].s.head != t[i + 3].s.head))
+        (p->in_type != p->out_type || (p->S > 1 && t[i].s.row != t[i + 3].s.row) ||
+         (t[i].heads > 1 && t[i].s.head != t[i + 3].s.head)))
       return DT_ERR_INVALID;
   for (const void* x : {(const void*)wq, (const void*)wk, (const void*)table, (const void*)q_mean, (const void*)k_mean})
     if (x && !aligned16(x)) return DT_ERR_UNSUPPORTED;

@@ -347,9 +347,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
   const uint64_t lim = p.wait_limit_ns;
   const int rank = p.split > 1 ? (int)cluster_rank() : 0;
 
-  if (warp == kWarpTma && lane == 0) {
-    for (int i = 0; i < C::kNumBars; ++i) mbar_init(&bars[i], C::arrivals(i));
-    *abort_flag = 0;
+  if (warp == kWarpTma) {
+    for (int i = lane; i < C::kNumBars; i += 32) mbar_init(&bars[i], C::arrivals(i));
+    if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async();
   }

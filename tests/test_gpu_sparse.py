@@ -173,6 +173,52 @@ def test_norm_rope_in_place_equals_out_of_place(ty, halves, S, H, Hkv, D):
     assert torch.equal(u[:H], Q) and torch.equal(u[H:H + Hkv], K) and torch.equal(y[:, H + Hkv:], x[:, H + Hkv:])
 
 
+def test_norm_rope_offsets_past_32_bits():
+    """An input and an output of more than 2^31 elements each: rows at both ends against the oracle."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = gen(25)
+    S, H, D = 700_001, 26, 128
+    x = torch.empty(S, H, D, dtype=BF, device="cuda")
+    for a in range(0, S, 100_000):
+        x[a:a + 100_000] = randn(g, min(100_000, S - a), H, D, dtype=BF)
+    t = x.transpose(0, 1)
+    ang = torch.rand(S, 8, generator=g, device="cuda") * 6
+    table = torch.stack([ang.cos(), ang.sin()], -1)
+    Q, qm = torch.empty(H, S, D, dtype=BF, device="cuda"), torch.empty(H, -(-S // 128), D, device="cuda")
+    assert x.numel() > 1 << 31 and Q.numel() > 1 << 31
+    p = dt.norm_rope_params(t, Q=Q, rot=16)
+    dt.dt_qk_norm_rope(p, t, None, None, None, None, table, Q, None, None, qm)
+    for h, a in ((0, 0), (H - 1, 0), (0, S - 65), (H - 1, S - 65), (13, 350_000 // 128 * 128)):
+        y, mag = sp.norm_rope(np64(t[h:h + 1, a:a + 65]), None, np64(table[a:a + 65]))
+        within(Q[h:h + 1, a:a + 65], y, 2.0 ** -19 * mag + HALF[BF] * (np.abs(y) + 2.0 ** -19 * mag), f"rows {a} of head {h}")
+    last = S // 128 * 128
+    y, mag = sp.norm_rope(np64(t[H - 1:, last:]), None, np64(table[last:]))
+    within(qm[H - 1:, -1:], sp.block_means(y, 128), (2.0 ** -19 + 128 * 2.0 ** -24) * sp.block_means(mag, 128), "last mean")
+
+
+def test_norm_and_select_at_once_on_two_streams():
+    g = gen(26)
+    q, k = randn(g, 8, 1000, 128, dtype=BF), randn(g, 8, 1000, 128, dtype=BF)
+    ang = torch.rand(1000, 64, generator=g, device="cuda")
+    table = torch.stack([ang.cos(), ang.sin()], -1)
+    out = []
+    torch.cuda.synchronize()
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream(), torch.cuda.Stream()):
+        Q, K = torch.empty_like(q), torch.empty_like(k)
+        qm, km = torch.empty(8, 8, 128, device="cuda"), torch.empty(8, 16, 128, device="cuda")
+        idx, count = torch.empty(8, 8, 5, dtype=torch.int32, device="cuda"), torch.empty(8, 8, dtype=torch.int32, device="cuda")
+        out.append((Q, K, qm, km, idx, count, s))
+    torch.cuda.synchronize()
+    p = dt.norm_rope_params(q, k, None, out[0][0], out[0][1], None, rot=128)
+    for Q, K, qm, km, idx, count, s in out:
+        dt.dt_qk_norm_rope(p, q, k, None, None, None, table, Q, K, None, qm, km, s)
+        dt.dt_block_select(dt.select_params(8, 8, 8, 16, 128, 5, 1, 0, 2.0), qm, km, idx, count, s)
+    torch.cuda.synchronize()
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0][:6], other[:6]))
+
+
 def test_norm_rope_odd_head_counts_mix_parts_in_a_warp():
     """Heads of all parts share warps when the counts are odd; infinities in one head stay there."""
     norm_case(130, 5, 3, 64, 64, False, BF, BF, seed=21)
