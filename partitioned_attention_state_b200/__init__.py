@@ -401,7 +401,9 @@ def _type_of(t) -> int:
 
 
 def _heads(t, name: str):
-    """(head, row) strides of a [heads][rows][D] tensor or view whose rows are contiguous."""
+    """(head, row) strides of a [heads][rows][D] tensor or view whose rows are contiguous; (0, 0) for None."""
+    if t is None:
+        return 0, 0
     st = t.stride()
     if len(st) != 3 or (st[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{name}: expected [heads][rows][D] with contiguous rows, got {tuple(t.shape)} "
@@ -409,32 +411,37 @@ def _heads(t, name: str):
     return st[:2]
 
 
-# The checks below run in every call, so they compare whole tuples and look closer only when those differ.
-def _match(t, shape, dtype, name: str, device: int) -> None:
-    """Raise unless t is a contiguous tensor of this shape and type on this device."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != device:
+# The two checks below run for every tensor of every call: they return its address (None for None) and look closer
+# only where the plain comparison fails.
+def _flat(t, shape, dtype, name: str, device: int):
+    """Address of t; raises unless t is a contiguous tensor of this shape and type on this device."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected contiguous {dtype} {shape} on device {device}, got {t.dtype} "
                          f"{tuple(t.shape)} with strides {t.stride()} on device {t.get_device()}")
+    return t.data_ptr()
 
 
-def _match_heads(t, shape, strides, dtype, name: str, device: int) -> None:
-    """Raise unless t is the [heads][rows][D] tensor that the parameters were made for."""
-    ok = t.shape == shape and t.dtype is dtype and t.get_device() == device
-    if ok:
-        st = t.stride()
-        ok = (st[0] == strides.head or shape[0] <= 1) and (st[1] == strides.row or shape[1] <= 1) and \
-             (st[2] == 1 or shape[2] <= 1)
-    if not ok:
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} on device {t.get_device()} is "
-                         f"not what the parameters describe: {dtype} {shape}, head stride {strides.head}, row stride "
-                         f"{strides.row}, on device {device}")
+def _strided(t, shape, strides, dtype, name: str, device: int):
+    """Address of t; raises unless t is the [heads][rows][D] tensor that the parameters were made for."""
+    if t is None:
+        return None
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device:
+        head, row, col = t.stride()
+        if (col == 1 or shape[2] <= 1) and (row == strides.row or shape[1] <= 1) and \
+                (head == strides.head or shape[0] <= 1):
+            return t.data_ptr()
+    raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} with strides {t.stride()} on device {t.get_device()} is "
+                     f"not what the parameters describe: {dtype} {shape}, head stride {strides.head}, row stride "
+                     f"{strides.row}, on device {device}")
 
 
 def _call(name: str, device: int, stream, p, *args) -> None:
     """One C call with the tensors' device current (launches go to the current device)."""
     if device < 0:
         raise ValueError(f"{name}: expected CUDA tensors")
-    f = getattr(load(), name)
+    f = getattr(_LIB or load(), name)
     if stream is None:          # the raw handle of the device's current stream, without a Stream object
         raw = _torch._C._cuda_getCurrentRawStream(device)
     else:
@@ -459,9 +466,8 @@ def rope_params(S: int, axes, base: float = 10000.0) -> RopeParams:
 def dt_rope_table(p: RopeParams, pos, table, stream=None) -> None:
     """pos: int32 [axes][S]; table: float32 [S][rot/2][2], written with (cos, sin)."""
     torch, dev, n = _init(), pos.get_device(), p.n_axes
-    _match(pos, (n, p.S), torch.int32, "pos", dev)
-    _match(table, (p.S, sum(p.dim[:n]) // 2, 2), torch.float32, "table", dev)
-    _call("dt_rope_table", dev, stream, p, pos.data_ptr(), table.data_ptr())
+    _call("dt_rope_table", dev, stream, p, _flat(pos, (n, p.S), torch.int32, "pos", dev),
+          _flat(table, (p.S, sum(p.dim[:n]) // 2, 2), torch.float32, "table", dev))
 
 
 def norm_rope_params(q=None, k=None, v=None, Q=None, K=None, V=None, rot: int = 0,
@@ -478,13 +484,11 @@ def norm_rope_params(q=None, k=None, v=None, Q=None, K=None, V=None, rot: int = 
     kv = k if k is not None else v
     _, S, D = first.shape
     ity = _type_of(first)
-    strides = []
-    for n, t in (("q", q), ("k", k), ("v", v), ("Q", Q), ("K", K), ("V", V)):
-        strides += (0, 0) if t is None else _heads(t, n)
     # packed in one go: setting the fields one by one costs as much as the launch
     return NormRopeParams.from_buffer_copy(_NORM_ROPE.pack(
         S, D, 0 if q is None else q.shape[0], 0 if kv is None else kv.shape[0], rot, pairing, ity,
-        ity if out is None else _type_of(out), int(norm), q_block, k_block, eps, *strides))
+        ity if out is None else _type_of(out), int(norm), q_block, k_block, eps, *_heads(q, "q"), *_heads(k, "k"),
+        *_heads(v, "v"), *_heads(Q, "Q"), *_heads(K, "K"), *_heads(V, "V")))
 
 
 def dt_qk_norm_rope(p: NormRopeParams, q, k, v, wq, wk, table, Q, K, V, q_mean=None, k_mean=None, stream=None) -> None:
@@ -495,35 +499,16 @@ def dt_qk_norm_rope(p: NormRopeParams, q, k, v, wq, wk, table, Q, K, V, q_mean=N
     first = q if q is not None else k if k is not None else v
     if first is None:
         raise ValueError("no input")
-    dev, S, D, rot = first.get_device(), p.S, p.D, p.rot
+    dev, S, D, rot, qb, kb = first.get_device(), p.S, p.D, p.rot, p.q_block, p.k_block
     qs, ks, ity, oty = (p.H, S, D), (p.Hkv, S, D), _TYPES.get(p.in_type), _TYPES.get(p.out_type)
-    ptr = []
-    for t, shape, st, n, ty in ((q, qs, p.q_in, "q", ity), (k, ks, p.k_in, "k", ity), (v, ks, p.v_in, "v", ity)):
-        if t is None:
-            ptr.append(None)
-        else:
-            _match_heads(t, shape, st, ty, n, dev)
-            ptr.append(t.data_ptr())
-    for t, shape, n in ((wq, (D,), "wq"), (wk, (D,), "wk"), (table if rot else None, (S, rot // 2, 2), "table")):
-        if t is None:
-            ptr.append(None)
-        else:
-            _match(t, shape, f32, n, dev)
-            ptr.append(t.data_ptr())
-    for t, shape, st, n, ty in ((Q, qs, p.q_out, "Q", oty), (K, ks, p.k_out, "K", oty), (V, ks, p.v_out, "V", oty)):
-        if t is None:
-            ptr.append(None)
-        else:
-            _match_heads(t, shape, st, ty, n, dev)
-            ptr.append(t.data_ptr())
-    for t, heads, block, n in ((q_mean, p.H, p.q_block, "q_mean"), (k_mean, p.Hkv, p.k_block, "k_mean")):
-        if t is None:
-            ptr.append(None)
-        else:
-            if block > 0:
-                _match(t, (heads, -(-S // block), D), f32, n, dev)
-            ptr.append(t.data_ptr())
-    _call("dt_qk_norm_rope", dev, stream, p, *ptr)
+    _call("dt_qk_norm_rope", dev, stream, p,
+          _strided(q, qs, p.q_in, ity, "q", dev), _strided(k, ks, p.k_in, ity, "k", dev),
+          _strided(v, ks, p.v_in, ity, "v", dev), _flat(wq, (D,), f32, "wq", dev), _flat(wk, (D,), f32, "wk", dev),
+          _flat(table, (S, rot // 2, 2), f32, "table", dev) if rot else None,
+          _strided(Q, qs, p.q_out, oty, "Q", dev), _strided(K, ks, p.k_out, oty, "K", dev),
+          _strided(V, ks, p.v_out, oty, "V", dev),
+          _flat(q_mean, (p.H, -(-S // qb) if qb > 0 else 0, D), f32, "q_mean", dev),
+          _flat(k_mean, (p.Hkv, -(-S // kb) if kb > 0 else 0, D), f32, "k_mean", dev))
 
 
 def select_params(H: int, Hkv: int, nq: int, nk: int, D: int, topk: int, keep_first: int = 0, keep_last: int = 0,
@@ -536,11 +521,9 @@ def dt_block_select(p: SelectParams, q_mean, k_mean, idx, count, stream=None) ->
     [H][nq][D], k_mean float32 [Hkv][nk][D]; idx int32 [H][nq][topk] and count
     int32 [H][nq] are written."""
     torch, dev, H, nq, D = _init(), q_mean.get_device(), p.H, p.nq, p.D
-    _match(q_mean, (H, nq, D), torch.float32, "q_mean", dev)
-    _match(k_mean, (p.Hkv, p.nk, D), torch.float32, "k_mean", dev)
-    _match(idx, (H, nq, p.topk), torch.int32, "idx", dev)
-    _match(count, (H, nq), torch.int32, "count", dev)
-    _call("dt_block_select", dev, stream, p, q_mean.data_ptr(), k_mean.data_ptr(), idx.data_ptr(), count.data_ptr())
+    _call("dt_block_select", dev, stream, p, _flat(q_mean, (H, nq, D), torch.float32, "q_mean", dev),
+          _flat(k_mean, (p.Hkv, p.nk, D), torch.float32, "k_mean", dev),
+          _flat(idx, (H, nq, p.topk), torch.int32, "idx", dev), _flat(count, (H, nq), torch.int32, "count", dev))
 
 
 def sparse_params(Q, K, V, O, k_block: int = 64, cap: int = 0) -> SparseParams:
@@ -560,20 +543,14 @@ def dt_attn_block_sparse(p: SparseParams, Q, K, V, idx, count, O, L, d_status, s
     [H][ceil(Sq/128)] or None (cap entries each), L float32 [H][Sq], d_status
     int32 device status word."""
     torch, dev, H, Sq, D = _init(), Q.get_device(), p.H, p.Sq, p.D
-    qs, ks, ty = (H, Sq, D), (p.Hkv, p.Sk, D), _TYPES.get(p.type)
-    _match_heads(Q, qs, p.q, ty, "Q", dev)
-    _match_heads(K, ks, p.k, ty, "K", dev)
-    _match_heads(V, ks, p.v, ty, "V", dev)
-    _match_heads(O, qs, p.o, _TYPES.get(p.out_type), "O", dev)
-    nqb = -(-Sq // DT_TILE)
-    _match(idx, (H, nqb, p.cap), torch.int32, "idx", dev)
-    if count is not None:
-        _match(count, (H, nqb), torch.int32, "count", dev)
-    _match(L, (H, Sq), torch.float32, "L", dev)
     if d_status.dtype is not torch.int32 or d_status.numel() < 1 or d_status.get_device() != dev:
         raise ValueError("d_status: expected an int32 tensor on the inputs' device")
-    _call("dt_attn_block_sparse", dev, stream, p, Q.data_ptr(), K.data_ptr(), V.data_ptr(), idx.data_ptr(),
-          None if count is None else count.data_ptr(), O.data_ptr(), L.data_ptr(), d_status.data_ptr())
+    qs, ks, ty, nqb = (H, Sq, D), (p.Hkv, p.Sk, D), _TYPES.get(p.type), -(-Sq // DT_TILE)
+    _call("dt_attn_block_sparse", dev, stream, p, _strided(Q, qs, p.q, ty, "Q", dev),
+          _strided(K, ks, p.k, ty, "K", dev), _strided(V, ks, p.v, ty, "V", dev),
+          _flat(idx, (H, nqb, p.cap), torch.int32, "idx", dev), _flat(count, (H, nqb), torch.int32, "count", dev),
+          _strided(O, qs, p.o, _TYPES.get(p.out_type), "O", dev), _flat(L, (H, Sq), torch.float32, "L", dev),
+          d_status.data_ptr())
 
 
 def dt_set_wait_limit_ns(ns: int) -> None:
