@@ -470,9 +470,9 @@ DT_API int dt_qk_norm_rope(const dt_norm_rope_params* p, const void* q, const vo
 #define DT_SELECT_MAX_BLOCKS 16384
 typedef struct {
   int32_t H, Hkv;               /* query heads; key heads: query head h reads key head h / (H/Hkv) */
-  int32_t nq, nk;               /* query blocks, key blocks (nk <= DT_SELECT_MAX_BLOCKS) */
+  int32_t nq, nk;               /* query blocks (at most 2^30), key blocks (nk <= DT_SELECT_MAX_BLOCKS) */
   int32_t D;                    /* a multiple of 4, 4 .. 128 */
-  int32_t topk;                 /* entries per list, >= 1 */
+  int32_t topk;                 /* entries per list, 1 .. 2^30 */
   int32_t keep_first, keep_last;/* the first and last key blocks that every list holds; sum <= topk */
   double margin;                /* >= 0; INFINITY: none */
 } dt_select_params;
@@ -497,10 +497,10 @@ DT_API int dt_block_select(const dt_select_params* p, const float* q_mean, const
 
 typedef struct {
   int32_t H, Hkv;               /* query heads; key heads: query head h reads key head h / (H/Hkv) */
-  int32_t Sq, Sk;               /* query rows, key rows */
+  int32_t Sq, Sk;               /* query rows, key rows: at most 2^30 */
   int32_t D;                    /* 64, 72 or 128 */
   int32_t k_block;              /* key rows per block: 64 or 128 */
-  int32_t cap;                  /* entries allocated per list */
+  int32_t cap;                  /* entries allocated per list, 0 .. 2^30 */
   int32_t type;                 /* of Q, K, V: DT_TYPE_BF16 or DT_TYPE_F16 */
   int32_t out_type;             /* of O: type, or DT_TYPE_F32 (OUT as dt_state_merge reads it) */
   dt_strides q, k, v, o;

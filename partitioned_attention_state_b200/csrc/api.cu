@@ -435,6 +435,8 @@ extern "C" int dt_block_select(const dt_select_params* p, const float* q_mean, c
   if (p->D < 4 || p->D > 128 || p->D % 4 != 0 || p->topk < 1) return DT_ERR_INVALID;
   if (p->keep_first < 0 || p->keep_last < 0 || (int64_t)p->keep_first + p->keep_last > p->topk) return DT_ERR_INVALID;
   if (!(p->margin >= 0.0)) return DT_ERR_INVALID;
+  // the kernel's 32-bit list and row counters run up to a warp past these
+  if (p->topk > 1 << 30 || p->nq > 1 << 30) return DT_ERR_INVALID;
   if (p->H > 0 && (p->Hkv < 1 || p->H % p->Hkv != 0)) return DT_ERR_INVALID;
   if ((int64_t)p->H * p->nq >= (int64_t)1 << 31) return DT_ERR_INVALID;
   if (p->nk > DT_SELECT_MAX_BLOCKS) return DT_ERR_UNSUPPORTED;
@@ -453,7 +455,8 @@ extern "C" int dt_attn_block_sparse(const dt_sparse_params* p, const void* Q, co
   if (!type_ok(p->type) || !type_ok(p->out_type)) return DT_ERR_INVALID;
   if (p->type == DT_TYPE_F32 || (p->out_type != p->type && p->out_type != DT_TYPE_F32)) return DT_ERR_UNSUPPORTED;
   if (p->D != 64 && p->D != 72 && p->D != 128) return DT_ERR_UNSUPPORTED;
-  if (p->Sq > 1 << 30 || p->Sk > 1 << 30) return DT_ERR_INVALID;
+  // 32-bit row and list counters run up to a tile (lists: 128 entries) past these
+  if (p->Sq > 1 << 30 || p->Sk > 1 << 30 || p->cap > 1 << 30) return DT_ERR_INVALID;
   const int nqb = dt::ceil_div(p->Sq, DT_TILE);
   if ((int64_t)p->H * nqb * 16 >= (int64_t)1 << 31) return DT_ERR_INVALID;
   if (p->H == 0 || p->Sq == 0) return DT_OK;

@@ -132,6 +132,12 @@ def test_select_limits_and_nothing_to_do():
     assert select(nq=0, idx=None) == dt.DT_OK
 
 
+@pytest.mark.parametrize("kw", [dict(topk=(1 << 30) + 1), dict(topk=2 ** 31 - 1), dict(H=1, Hkv=1, nq=(1 << 30) + 1),
+                                dict(H=1, Hkv=1, nq=2 ** 31 - 1)])
+def test_select_refuses_sizes_that_index_sums_would_pass(kw):
+    assert select(**kw) == dt.DT_ERR_INVALID
+
+
 # ------------------------------------------------------------------ attention
 SP = dict(H=4, Hkv=2, Sq=100, Sk=200, D=64, k_block=64, cap=3, type=0, out_type=0)
 
@@ -150,6 +156,12 @@ def attend(ptrs=None, strides=None, **over):
                                 dict(out_type=7), dict(H=1 << 24, Hkv=1, Sq=1 << 10)])
 def test_attention_refuses_parameters(kw):
     assert attend(**kw) == dt.DT_ERR_INVALID
+
+
+@pytest.mark.parametrize("cap", [(1 << 30) + 1, 2 ** 31 - 1])
+@pytest.mark.parametrize("k_block", [64, 128])
+def test_attention_refuses_lists_that_index_sums_would_pass(cap, k_block):
+    assert attend(cap=cap, k_block=k_block) == dt.DT_ERR_INVALID
 
 
 @pytest.mark.parametrize("kw", [dict(D=32), dict(D=80), dict(D=256), dict(type=2, out_type=2), dict(out_type=1)])
