@@ -460,7 +460,8 @@ typedef struct {
  *               consecutive rows (the last block: of the rows it has), of the
  *               values before the rounding to out_type
  *   k_mean      fp32 [Hkv][ceil(S/k_block)][D] or NULL
- * Row starts must be 16-byte aligned (pointers and strides); strides >= 0.
+ * Row starts must be 16-byte aligned (pointers and strides); strides of
+ * inputs >= 0 (0: broadcast), of outputs > 0.
  * S = 0 launches nothing.  One launch, HBM-bound.  Errors: DT_ERR_INVALID,
  * DT_ERR_UNSUPPORTED (alignment, types), DT_ERR_CUDA. */
 DT_API int dt_qk_norm_rope(const dt_norm_rope_params* p, const void* q, const void* k, const void* v,

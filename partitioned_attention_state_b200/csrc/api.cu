@@ -328,8 +328,8 @@ bool type_ok(int t) { return t == DT_TYPE_BF16 || t == DT_TYPE_F16 || t == DT_TY
 bool strides_aligned(const dt_strides& s, int heads, int rows, int size) {
   return (heads <= 1 || s.head * size % 16 == 0) && (rows <= 1 || s.row * size % 16 == 0);
 }
-bool strides_nonneg(const dt_strides& s, int heads, int rows) {
-  return (heads <= 1 || s.head >= 0) && (rows <= 1 || s.row >= 0);
+bool strides_from(int64_t least, const dt_strides& s, int heads, int rows) {
+  return (heads <= 1 || s.head >= least) && (rows <= 1 || s.row >= least);
 }
 
 // 16-bit [heads][S][D] with element strides as a 3-D tensor (D, S, heads); box (bw, rows, 1)
@@ -404,7 +404,8 @@ extern "C" int dt_qk_norm_rope(const dt_norm_rope_params* p, const void* q, cons
       {K, p->k_out, p->Hkv, type_size(p->out_type)}, {V, p->v_out, p->Hkv, type_size(p->out_type)}};
   for (const auto& x : t)
     if (x.p) {
-      if (!strides_nonneg(x.s, x.heads, p->S)) return DT_ERR_INVALID;
+      // a stride of 0 broadcasts an input; rows of an output would overwrite one another
+      if (!strides_from(&x < t + 3 || p->S == 0 ? 0 : 1, x.s, x.heads, p->S)) return DT_ERR_INVALID;
       if (!aligned16(x.p) || !strides_aligned(x.s, x.heads, p->S, x.size)) return DT_ERR_UNSUPPORTED;
     }
   // in place: each element is read and written by one thread only if both sides are laid out alike

@@ -106,6 +106,20 @@ def test_norm_rope_in_place_needs_the_same_layout():
     assert norm_rope(one, strides=dict(q_out=dt.Strides(1280, 64))) == dt.DT_ERR_INVALID
 
 
+def test_norm_rope_output_rows_do_not_share_memory():
+    """A stride of 0 broadcasts an input; as an output's it would have rows or heads overwrite one another."""
+    for n in ("q_out", "k_out", "v_out"):
+        assert norm_rope(strides={n: dt.Strides(640, 0)}) == dt.DT_ERR_INVALID, n
+        assert norm_rope(strides={n: dt.Strides(0, 64)}) == dt.DT_ERR_INVALID, n
+    # in place on a broadcast input
+    one = {**{n: None for n in NAMES}, "q": P, "Q": P, "wq": P, "table": P}
+    for st in (dt.Strides(640, 0), dt.Strides(0, 64)):
+        assert norm_rope(one, strides=dict(q_in=st, q_out=st)) == dt.DT_ERR_INVALID
+    # nothing to write: no rows share memory
+    apart = dict(Q=P + 4096, K=P + 8192, V=P + 12288)
+    assert norm_rope(apart, S=0, strides={n: dt.Strides(0, 0) for n in ("q_out", "k_out", "v_out")}) == dt.DT_OK
+
+
 # ------------------------------------------------------------------ selection
 SEL = dict(H=4, Hkv=2, nq=3, nk=5, D=64, topk=2, keep_first=0, keep_last=0, margin=float("inf"))
 
