@@ -135,11 +135,21 @@ class Session:
                 dst.copy_(src)
         self._measured = None
 
-    def _use_means(self, k_block: int) -> None:
+    def _on(self, stream):
+        """Context in which `stream` (a torch stream, a raw handle, None: as it is) is the current one.  What a call
+        allocates for launches on `stream` has to come from that stream's pool: memory handed out on another one may
+        still be read by work that is pending there."""
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raw = getattr(stream, "cuda_stream", stream)
+            stream = torch.cuda.ExternalStream(raw, self.device) if raw else torch.cuda.default_stream(self.device)
+        return torch.cuda.stream(stream)
+
+    def _use_means(self, k_block: int, stream) -> None:
         if k_block not in self._means:
-            self._means[k_block] = tuple(
-                torch.empty((self.H, -(-self.S // block), self.D), dtype=torch.float32, device=self.device)
-                for block in (DT_TILE, k_block))
+            with self._on(stream):
+                self._means[k_block] = tuple(
+                    torch.empty((self.H, -(-self.S // block), self.D), dtype=torch.float32, device=self.device)
+                    for block in (DT_TILE, k_block))
         self.q_mean, self.k_mean = self._means[k_block]
 
     def set_projection(self, qkv: torch.Tensor, wq=None, wk=None, table=None, pairing: int = DT_ROPE_INTERLEAVED,
@@ -155,7 +165,7 @@ class Session:
         x = qkv.unflatten(1, (3, self.H, self.D)).permute(1, 2, 0, 3)
         if k_block not in (64, 128):
             raise ValueError(f"k_block: 64 or 128, got {k_block}")
-        self._use_means(k_block)
+        self._use_means(k_block, stream)
         p = norm_rope_params(x[0], x[1], x[2], self.Q, self.K, self.V, rot=0 if table is None else 2 * table.shape[1],
                              pairing=pairing, norm=norm, eps=eps, q_block=DT_TILE, k_block=k_block)
         dt_qk_norm_rope(p, x[0], x[1], x[2], wq, wk, table, self.Q, self.K, self.V, self.q_mean, self.k_mean, stream)
@@ -260,7 +270,7 @@ class Session:
             raise ValueError(f"k_block: 64 or 128, got {k_block}")
         if not remeasure and self._measured != k_block:
             raise ValueError("remeasure=False needs the block means of set_projection with this k_block")
-        self._use_means(k_block)
+        self._use_means(k_block, stream)
         if remeasure:
             p = norm_rope_params(self.Q, self.K, norm=False, q_block=DT_TILE, k_block=k_block)
             dt_qk_norm_rope(p, self.Q, self.K, None, None, None, None, None, None, None, self.q_mean, self.k_mean, stream)
@@ -268,8 +278,9 @@ class Session:
         nq, nk = self.q_mean.shape[1], self.k_mean.shape[1]
         sel = select_params(self.H, self.H, nq, nk, self.D, topk, keep_first, keep_last, margin)
         if topk not in self._lists:
-            self._lists[topk] = (torch.empty((self.H, nq, topk), dtype=torch.int32, device=self.device),
-                                 torch.empty((self.H, nq), dtype=torch.int32, device=self.device))
+            with self._on(stream):
+                self._lists[topk] = (torch.empty((self.H, nq, topk), dtype=torch.int32, device=self.device),
+                                     torch.empty((self.H, nq), dtype=torch.int32, device=self.device))
         self.lists = idx, count = self._lists[topk]
         dt_block_select(sel, self.q_mean, self.k_mean, idx, count, stream)
         dt_attn_block_sparse(sparse_params(self.Q, self.K, self.V, self.O, k_block, topk), self.Q, self.K, self.V, idx,

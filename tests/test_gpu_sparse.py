@@ -804,3 +804,30 @@ def test_session_sparse_steps_of_several_sizes_beside_a_captured_one():
     graph.replay()
     sess.check()
     assert torch.equal(sess.O, want_o) and torch.equal(lists[0], want_l)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_session_buffers_of_a_first_call_belong_to_its_stream(raw):
+    """The first set_projection and step_sparse of a size, on a stream of their own while the current stream is busy:
+    memory freed on the current stream, which its pending work still reads, is not handed to them."""
+    g = gen(71)
+    H, S, D, topk = 4, 1000, 64, 5
+    qkv = randn(g, S, 3 * H * D, dtype=BF)
+    ref = Session(H, S, D, P=2, cache=False)
+    ref.set_projection(qkv)
+    ref.step_sparse(topk, remeasure=False)
+    sess, side = Session(H, S, D, P=2, cache=False), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    nq, nk = -(-S // 128), -(-S // 64)
+    old = [torch.full((n,), 5.0, device="cuda") for n in (H * nq * D, H * nk * D, H * nq * topk, H * nq)]
+    seen = [torch.empty_like(t) for t in old]
+    torch.cuda._sleep(100_000_000)                    # the copies below stay pending for tens of milliseconds
+    for t, u in zip(old, seen):
+        u.copy_(t)
+    del old, t
+    stream = side.cuda_stream if raw else side
+    sess.set_projection(qkv, stream=stream)
+    sess.step_sparse(topk, remeasure=False, stream=stream)
+    torch.cuda.synchronize()
+    assert all(bool((u == 5.0).all()) for u in seen)
+    assert torch.equal(sess.O, ref.O) and torch.equal(sess.L, ref.L) and torch.equal(sess.lists[0], ref.lists[0])
