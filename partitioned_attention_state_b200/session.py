@@ -226,9 +226,10 @@ class Session:
         self._mark_plan_read(st)
         w = None
         if anchored:
-            d_w = torch.empty((max(self.nqt, 1), self.nseg), dtype=torch.float32, device=self.device)
-            dt_state_importance(p, self.cache_L, self.L, d_w, self.status, st)
-            w = d_w[: self.nqt].cpu().numpy()
+            with self._on(st):                   # allocated, written and read back in the launch's order
+                d_w = torch.empty((max(self.nqt, 1), self.nseg), dtype=torch.float32, device=self.device)
+                dt_state_importance(p, self.cache_L, self.L, d_w, self.status, st)
+                w = d_w[: self.nqt].cpu().numpy()
         st.synchronize()
         self.check()
         err = self.d_err[: self.nqt].cpu().numpy()

@@ -742,3 +742,24 @@ def test_anchor_guided_schedule_matches_oracle(g, sd):
         reused.append(int((plan == orc.REUSE).sum()))
     assert anchors[0] and anchors[5] and not any(anchors[1:5])
     assert reused[1] > 0 and reused[6] > 0              # steps after an anchor reuse states
+
+
+def test_session_anchor_step_on_a_side_stream():
+    """An anchor-guided step on a stream that is behind the current one: the importance is read back after it is
+    measured, and planning goes on as on the current stream."""
+    H, S, D, P = 2, 1024, 64, 4
+    sessions = [Session(H, S, D, P, mode=dt.DT_MODE_ANCHOR) for _ in range(2)]
+    s = stream_of(H, S, D, 0.05, seed=5)
+    side = torch.cuda.Stream()
+    for step in range(1, 4):
+        q, k, v = s()
+        for sess in sessions:
+            sess.set_inputs(q, k, v)
+        torch.cuda.synchronize()
+        want = sessions[0].step(step)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)
+        assert sessions[1].step(step, stream=side) == want
+        assert np.array_equal(sessions[0].weights, sessions[1].weights) and sessions[0].weights.max() > 0
+        assert np.array_equal(sessions[0].last_plan, sessions[1].last_plan)
+        assert torch.equal(sessions[0].O, sessions[1].O)
