@@ -88,7 +88,7 @@ class Session:
             self.last_anchored = False
         self.last_counts = None
         self.last_plan = None
-        # block means and lists of sparse steps, one buffer per k_block and per topk, kept: a captured graph goes on
+        # block means (per k_block) and lists (per k_block and topk) of sparse steps, kept: a captured graph goes on
         # using the ones it was captured with
         self._means: dict = {}
         self._lists: dict = {}
@@ -278,11 +278,12 @@ class Session:
             self._measured = k_block
         nq, nk = self.q_mean.shape[1], self.k_mean.shape[1]
         sel = select_params(self.H, self.H, nq, nk, self.D, topk, keep_first, keep_last, margin)
-        if topk not in self._lists:
+        if (k_block, topk) not in self._lists:
             with self._on(stream):
-                self._lists[topk] = (torch.empty((self.H, nq, topk), dtype=torch.int32, device=self.device),
-                                     torch.empty((self.H, nq), dtype=torch.int32, device=self.device))
-        self.lists = idx, count = self._lists[topk]
+                self._lists[k_block, topk] = (
+                    torch.empty((self.H, nq, topk), dtype=torch.int32, device=self.device),
+                    torch.empty((self.H, nq), dtype=torch.int32, device=self.device))
+        self.lists = idx, count = self._lists[k_block, topk]
         dt_block_select(sel, self.q_mean, self.k_mean, idx, count, stream)
         dt_attn_block_sparse(sparse_params(self.Q, self.K, self.V, self.O, k_block, topk), self.Q, self.K, self.V, idx,
                              count, self.O, self.L, self.status, stream)

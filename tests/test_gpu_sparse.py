@@ -831,3 +831,25 @@ def test_session_buffers_of_a_first_call_belong_to_its_stream(raw):
     torch.cuda.synchronize()
     assert all(bool((u == 5.0).all()) for u in seen)
     assert torch.equal(sess.O, ref.O) and torch.equal(sess.L, ref.L) and torch.equal(sess.lists[0], ref.lists[0])
+
+
+def test_session_lists_of_two_block_sizes_and_one_length():
+    """The same topk with both block sizes: neither step overwrites the other's lists, captured or not."""
+    g = gen(73)
+    H, S, D, topk = 2, 1000, 64, 4
+    sess = Session(H, S, D, P=2, cache=False)
+    sess.set_inputs(*(randn(g, H, S, D, dtype=BF) for _ in range(3)))
+    sess.step_sparse(topk, k_block=64)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sess.step_sparse(topk, k_block=64)
+    lists = sess.lists
+    graph.replay()
+    want = [t.clone() for t in lists]
+    sess.step_sparse(topk, k_block=128)
+    other, want_other = sess.lists, [t.clone() for t in sess.lists]
+    assert all(torch.equal(a, b) for a, b in zip(lists, want))
+    graph.replay()
+    sess.check()
+    assert all(torch.equal(a, b) for a, b in zip(other, want_other))
+    assert all(torch.equal(a, b) for a, b in zip(lists, want))
