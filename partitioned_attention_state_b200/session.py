@@ -93,6 +93,7 @@ class Session:
         self._means: dict = {}
         self._lists: dict = {}
         self._measured: Optional[int] = None  # k_block for which the means are those of the current Q and K
+        self._captured: Optional[int] = None  # k_block of the means that the work captured last will leave
         self.q_mean = self.k_mean = None      # means of the last set_projection or step_sparse
         self.lists = None                     # (idx, count) of the last step_sparse
 
@@ -133,7 +134,7 @@ class Session:
                 dst.copy_(bf16_from_bits(src, "cpu"))
             else:
                 dst.copy_(src)
-        self._measured = None
+        self._measured = self._captured = None
 
     def _on(self, stream):
         """Context in which `stream` (a torch stream, a raw handle, None: as it is) is the current one.  What a call
@@ -152,6 +153,27 @@ class Session:
                     for block in (DT_TILE, k_block))
         self.q_mean, self.k_mean = self._means[k_block]
 
+    def _capturing(self, stream) -> bool:
+        with self._on(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+    def _means_left(self, k_block: int, capturing: bool) -> None:
+        """Note that the work just issued leaves the means of k_block; captured work has not run yet."""
+        if capturing:
+            self._captured = k_block
+            if self._measured != k_block:            # a replay will change Q and K under the means at hand
+                self._measured = None
+        else:
+            self._measured, self._captured = k_block, None
+
+    def declare_means(self, k_block: Optional[int]) -> None:
+        """Which block means are those of Q and K as they now are, where the session cannot know: k_block after a
+        replayed graph ran set_projection or a step_sparse that measured, None after anything else (a replayed
+        set_inputs, a write into Q or K) changed them.  step_sparse(remeasure=False) goes by it."""
+        if k_block is not None and k_block not in self._means:
+            raise ValueError(f"block means for k_block {k_block} were never measured or captured")
+        self._measured = k_block
+
     def set_projection(self, qkv: torch.Tensor, wq=None, wk=None, table=None, pairing: int = DT_ROPE_INTERLEAVED,
                        norm: bool = True, eps: float = 1e-6, k_block: int = 64, stream=None) -> None:
         """Inputs from the layer's packed projection (dt_qk_norm_rope): qkv
@@ -169,7 +191,7 @@ class Session:
         p = norm_rope_params(x[0], x[1], x[2], self.Q, self.K, self.V, rot=0 if table is None else 2 * table.shape[1],
                              pairing=pairing, norm=norm, eps=eps, q_block=DT_TILE, k_block=k_block)
         dt_qk_norm_rope(p, x[0], x[1], x[2], wq, wk, table, self.Q, self.K, self.V, self.q_mean, self.k_mean, stream)
-        self._measured = k_block
+        self._means_left(k_block, self._capturing(stream))
 
     # -------------------------------------------------------------- planning
     def plan(self, step: int, mode: Optional[int] = None, explicit: Optional[np.ndarray] = None):
@@ -265,17 +287,21 @@ class Session:
         (keep_first, keep_last, margin: see there).  The state cache, the
         stamps and the plan are left alone.  remeasure=False takes the block
         means that set_projection (same k_block) left, which is right as long as
-        Q and K are what it wrote; else they are measured first.  The lists
-        stay in ``lists`` (idx, count)."""
+        Q and K are what it wrote; else they are measured first.  The session
+        sees what is issued, not what a graph replays: while a capture is under
+        way, the means may be those of a captured set_projection, and after a
+        replay that wrote Q or K, declare_means says which are right.  The
+        lists stay in ``lists`` (idx, count)."""
         if k_block not in (64, 128):
             raise ValueError(f"k_block: 64 or 128, got {k_block}")
-        if not remeasure and self._measured != k_block:
+        capturing = self._capturing(stream)
+        if not remeasure and self._measured != k_block and not (capturing and self._captured == k_block):
             raise ValueError("remeasure=False needs the block means of set_projection with this k_block")
         self._use_means(k_block, stream)
         if remeasure:
             p = norm_rope_params(self.Q, self.K, norm=False, q_block=DT_TILE, k_block=k_block)
             dt_qk_norm_rope(p, self.Q, self.K, None, None, None, None, None, None, None, self.q_mean, self.k_mean, stream)
-            self._measured = k_block
+            self._means_left(k_block, capturing)
         nq, nk = self.q_mean.shape[1], self.k_mean.shape[1]
         sel = select_params(self.H, self.H, nq, nk, self.D, topk, keep_first, keep_last, margin)
         if (k_block, topk) not in self._lists:
@@ -311,7 +337,7 @@ class Session:
         made to wait for, everything issued here: synchronise the current
         stream before reading o and lse.  Returns the plan counts."""
         dev = self.device
-        self._measured = None
+        self._measured = self._captured = None
         cur = torch.cuda.current_stream(dev)
         if getattr(self, "_host_streams", None) is None:
             self._host_streams = tuple(torch.cuda.Stream(dev) for _ in range(3))

@@ -853,3 +853,59 @@ def test_session_lists_of_two_block_sizes_and_one_length():
     sess.check()
     assert all(torch.equal(a, b) for a, b in zip(other, want_other))
     assert all(torch.equal(a, b) for a, b in zip(lists, want))
+
+
+def test_session_block_means_of_captured_projections():
+    """A captured set_projection measures nothing until it is replayed, and a replay is not seen by the session:
+    remeasure=False takes the means that ran last or were declared."""
+    g = gen(79)
+    H, S, D = 2, 900, 64
+    qkv = randn(g, S, 3 * H * D, dtype=BF)
+    ref = Session(H, S, D, P=2, cache=False)
+    ref.set_projection(qkv)
+    ref.step_sparse(5, remeasure=False)
+    torch.cuda.synchronize()
+    sess = Session(H, S, D, P=2, cache=False)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sess.set_projection(qkv)
+        sess.step_sparse(5, remeasure=False)          # what the replay measures before it
+    with pytest.raises(ValueError):
+        sess.step_sparse(5, remeasure=False)          # nothing has run
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(sess.O, ref.O)
+    sess.declare_means(64)
+    sess.O.zero_()
+    sess.step_sparse(5, remeasure=False)
+    sess.check()
+    assert torch.equal(sess.O, ref.O) and torch.equal(sess.lists[0], ref.lists[0])
+    # a replay after an eager projection with the other block size, and after inputs set directly
+    sess.set_projection(-2 * qkv, k_block=128)
+    sess.step_sparse(5, remeasure=False, k_block=128)
+    graph.replay()
+    sess.declare_means(64)
+    with pytest.raises(ValueError):
+        sess.step_sparse(5, remeasure=False, k_block=128)
+    sess.step_sparse(5, remeasure=False)
+    sess.check()
+    assert torch.equal(sess.O, ref.O)
+    sess.set_inputs(ref.Q, ref.K, ref.V)
+    with pytest.raises(ValueError):
+        sess.step_sparse(5, remeasure=False)
+    sess.set_projection(qkv)
+    sess.declare_means(None)                          # Q or K changed behind the session's back
+    with pytest.raises(ValueError):
+        sess.step_sparse(5, remeasure=False)
+    # a captured projection with another block size leaves no eager claim behind
+    sess.set_projection(qkv)
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        sess.set_projection(qkv, k_block=128)
+    for k_block in (64, 128):
+        with pytest.raises(ValueError):
+            sess.step_sparse(5, remeasure=False, k_block=k_block)
+    for bad in (96, 0):
+        with pytest.raises(ValueError):
+            sess.declare_means(bad)
+    with pytest.raises(ValueError):
+        Session(H, S, D, P=2, cache=False).declare_means(64)      # never measured
