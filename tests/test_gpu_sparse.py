@@ -909,3 +909,48 @@ def test_session_block_means_of_captured_projections():
             sess.declare_means(bad)
     with pytest.raises(ValueError):
         Session(H, S, D, P=2, cache=False).declare_means(64)      # never measured
+
+
+# ------------------------------------------------------------------ fp32 states
+def attend_f32(q, k, v, idx, count, block, token_major):
+    """O as fp32, dense or token-major (head-major view of [Sq][H][D])."""
+    H, Sq, D = q.shape
+    o = torch.full((Sq, H, D), 9.0, device="cuda").transpose(0, 1) if token_major else None
+    O, L, st = attend(q, k, v, idx, count, block, oty=F32, o=o)
+    assert st == 0
+    check_attention(q, k, v, idx, count, block, O, L)
+
+
+@pytest.mark.parametrize("ty", [BF, FP])
+@pytest.mark.parametrize("D", [64, 72, 128])
+@pytest.mark.parametrize("H,Hkv,Sq,Sk,block,cap", [(1, 1, 1, 1, 64, 1), (2, 1, 129, 200, 128, 2), (4, 2, 300, 1000, 64, 7),
+                                                   (3, 3, 257, 777, 128, 5), (2, 1, 17, 4100, 64, 65)])
+def test_fp32_states_sizes(ty, D, H, Hkv, Sq, Sk, block, cap):
+    g = gen(Sq + Sk + 1)
+    q, k, v = randn(g, H, Sq, D, dtype=ty), randn(g, Hkv, Sk, D, dtype=ty), randn(g, Hkv, Sk, D, dtype=ty)
+    for counts, token_major in ((cap, False), (RAGGED(cap), True), (0, True)):
+        idx, count = lists_for(g, H, Sq, Sk, block, cap, counts)
+        attend_f32(q, k, v, idx, count, block, token_major)
+
+
+@pytest.mark.parametrize("ty", [BF, FP])
+@pytest.mark.parametrize("D", [64, 72, 128])
+@pytest.mark.parametrize("H,Sq,cap", [(1, 1, 33), (5, 130, 30), (20, 100, 64), (74, 3, 8)])
+def test_fp32_states_of_lists_split_over_a_cluster(ty, D, H, Sq, cap):
+    g = gen(83)
+    block, Sk = 64, 64 * 64
+    q, k, v = randn(g, H, Sq, D, dtype=ty), randn(g, 1, Sk, D, dtype=ty), randn(g, 1, Sk, D, dtype=ty)
+    for counts, token_major in ((cap, True), (RAGGED(cap), False), (1, False)):
+        idx, count = lists_for(g, H, Sq, Sk, block, cap, counts)
+        attend_f32(q, k, v, idx, count, block, token_major)
+
+
+@pytest.mark.parametrize("ty", [BF, FP])
+@pytest.mark.parametrize("H,Hkv,Sq,D,block", [(40, 40, 600, 128, 64), (160, 20, 128, 64, 128), (30, 30, 700, 72, 64)])
+def test_fp32_states_of_many_items_per_cta(ty, H, Hkv, Sq, D, block):
+    g = gen(89)
+    Sk, cap = 1500, 9
+    q, k, v = randn(g, H, Sq, D, dtype=ty), randn(g, Hkv, Sk, D, dtype=ty), randn(g, Hkv, Sk, D, dtype=ty)
+    idx, count = lists_for(g, H, Sq, Sk, block, cap, RAGGED(cap))
+    for token_major in (False, True):
+        attend_f32(q, k, v, idx, count, block, token_major)
