@@ -421,11 +421,12 @@ typedef struct {
 
 /* Rotation table: pair i of axis a (j-th pair of that axis, axes in order) of
  * token s turns by pos[a][s] * base^(-2 j / dim[a]); table[s][i] = (cos, sin).
- * The fraction of a turn is formed in 64 bits, so far positions keep theirs.
+ * The fraction of a turn is formed in 64 bits, so far positions keep theirs:
+ * results are within 2^-22 + 2 pi |pos| 2^-58.
  *   pos     int32 [n_axes][S] (device, read; any sign)
  *   table   fp32 [S][rot/2][2] (device, written)
- * One launch, HBM-bound.  S = 0 launches nothing.  Errors: DT_ERR_INVALID,
- * DT_ERR_UNSUPPORTED (misaligned pointer), DT_ERR_CUDA. */
+ * One launch, bound by its instructions.  S = 0 launches nothing.  Errors:
+ * DT_ERR_INVALID, DT_ERR_UNSUPPORTED (misaligned pointer), DT_ERR_CUDA. */
 DT_API int dt_rope_table(const dt_rope_params* p, const int32_t* pos, float* table, void* stream);
 
 #define DT_ROPE_INTERLEAVED 0   /* rotation pairs (2i, 2i+1) */

@@ -369,7 +369,7 @@ extern "C" int dt_rope_table(const dt_rope_params* p, const int32_t* pos, float*
   a.table = table;
   a.S = p->S;
   for (int x = 0; x < p->n_axes; ++x) {
-    // powers of one ratio: 128 extended-precision products stay below 2^-56
+    // powers of one ratio: at most 127 extended-precision products, and the truncation, stay below 2^-58
     const long double ratio = powl((long double)p->base, -2.0L / p->dim[x]);
     long double t = 1.0L / 6.283185307179586476925L;
     for (int j = 0; j < p->dim[x] / 2; ++j, t *= ratio) {

@@ -27,11 +27,14 @@ int cdiv(int a, int b) { return (a + b - 1) / b; }
 // ------------------------------------------------------------------ rotation table
 // cos and sin of 2 pi t, t = pos * turns, where only t's fraction counts: with
 // turns as a 64-bit binary fraction T, pos * T mod 2^64 is that fraction
-// without any reduction, off by at most |pos| 2^-65 turns, and needs no 64-bit
-// floating point.  Its upper 32 bits split into the nearest quarter turn and a
+// without any reduction, and needs no 64-bit floating point.  T is off by less
+// than 2^-58 (truncation 2^-64; at most 127 extended-precision products of one
+// power: 0.16 e^-z (3 * 127 + z + 2) 2^-64, z = -ln of the frequency), so the
+// farthest position by less than 2^-27 turns.  Its upper 32 bits split into the nearest quarter turn and a
 // rest |x| <= 1/8 turn, on which sin(2 pi x) / x and cos(2 pi x) are
 // polynomials in x^2 (minimax by Remez exchange: 1.3e-9 and 5e-11), two pairs in
-// each packed operation.  With the rounding of x the results are within 2^-23.
+// each packed operation.  The roundings of x (2 pi 2^-28) and of the polynomials
+// leave the results within 2^-22 by bound, 2^-23.2 as measured, near and far.
 // A CTA owns kRopeTokens tokens, a thread two pairs of a token (16 bytes of the
 // table) at a time; T and the axes lie in shared memory, since lanes with
 // different pairs would serialise on the parameter bank.  The library's sincospif and

@@ -9,6 +9,7 @@ import math
 import os
 import subprocess
 import sys
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -954,3 +955,45 @@ def test_fp32_states_of_many_items_per_cta(ty, H, Hkv, Sq, D, block):
     idx, count = lists_for(g, H, Sq, Sk, block, cap, RAGGED(cap))
     for token_major in (False, True):
         attend_f32(q, k, v, idx, count, block, token_major)
+
+
+# ------------------------------------------------------------------ far rotations
+TWO_PI = Decimal("6.28318530717958647692528676655900576839433879875021164194988918")
+
+
+def rope_table_60_digits(pos, dims, base):
+    """(cos, sin) with the turns and their reduction in 60 digits; off by less than 2^-49."""
+    with localcontext() as ctx:
+        ctx.prec = 60
+        cols = []
+        for p, dim in zip(pos, dims):
+            for j in range(dim // 2):
+                turn = Decimal(base) ** (Decimal(-2 * j) / dim) / TWO_PI
+                cols.append([float(x - x.to_integral_value()) for x in (int(v) * turn for v in p)])
+    angle = 2 * np.pi * np.array(cols).T
+    return np.stack([np.cos(angle), np.sin(angle)], axis=-1)
+
+
+def test_the_60_digit_oracle_is_the_tables_formula():
+    pos = np.array([[0, 1, -7, 1000], [3, -2, 11, 0]])
+    ref, _ = sp.rope_table(pos, (12, 8), 10000.0)
+    np.testing.assert_allclose(rope_table_60_digits(pos, (12, 8), 10000.0), ref, atol=1e-12)
+
+
+@pytest.mark.parametrize("axes,base", [((128,), 10000.0), ((256,), 2.0), ((44, 42, 42), 1e6), ((6, 10), 10000.0),
+                                       ((64, 2), 1.0), ((72,), 500000.0), ((256,), 1.01), ((40, 4), 1e300)])
+def test_rope_table_far_positions(axes, base):
+    """Positions to both ends of int32, against angles reduced in 60 digits.
+
+    A frequency is held within 2^-58 of a turn: truncation takes 2^-64, and at most 127 extended-precision products
+    with a power that is itself within two units leave 0.16 e^-z (3 * 127 + z + 2) 2^-64 < 2^-58, z = the frequency's
+    negative logarithm.  The reduced angle's rounding takes 2 pi 2^-28, the polynomials and their evaluation at most
+    three roundings of values below 1: 2^-22 in all."""
+    g = np.random.Generator(np.random.PCG64(len(axes)))
+    far = [-2 ** 31, -2 ** 31 + 1, 2 ** 31 - 1, 2 ** 31 - 2, -2 ** 30 - 12345, 2 ** 30 + 54321, -1, 0, 1, -131071, 1 << 20]
+    pos = np.array([np.concatenate([np.roll(far, a), g.integers(-2 ** 31, 2 ** 31, 20)]) for a in range(len(axes))])
+    table = torch.empty(pos.shape[1], sum(axes) // 2, 2, device="cuda")
+    dt.dt_rope_table(dt.rope_params(pos.shape[1], axes, base), torch.from_numpy(pos.astype(np.int32)).cuda(), table)
+    axis = np.repeat(np.arange(len(axes)), np.array(axes) // 2)
+    bound = 2.0 ** -22 + 2 * np.pi * 2.0 ** -58 * np.abs(pos[axis].T.astype(np.float64))
+    within(table, rope_table_60_digits(pos, axes, base), bound[..., None], "table")
