@@ -44,7 +44,10 @@
 //
 // P is rounded to the 16-bit type of V for the tensor cores (by at most 2^-8 of
 // a weight in bf16, 2^-11 in fp16, with signs that average out over a row's keys);
-// sums, maxima and O stay in fp32, and l sums the unrounded weights.
+// sums, maxima and O stay in fp32, and l sums the unrounded weights.  In fp16 the
+// weights are scaled by 2^7, as far as the range allows with a reference that lags
+// by 2^8: unscaled, weights below 2^-25 of the row's heaviest rounded to nothing,
+// and with them up to 2^-25 of O per key of a long list.
 //
 // Every wait is bounded; one that runs out raises an abort flag shared by all
 // roles and writes DT_ERR_TIMEOUT to *status, and every role drains its
@@ -78,6 +81,10 @@ constexpr int kMaxSplit = 16;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kLead = 8;                    // tiles of an item left to load when the next item is taken
 constexpr float kRescaleThreshold = 8.0f;   // log2 units: rescale O only when the max grows by > 2^8
+// log2 of the scale of P: the reference maximum stands this far below the row's.  2^(7 + 8) is in fp16's range; bf16
+// has the exponents of fp32.
+template <bool F16>
+constexpr float kLift = F16 ? 7.0f : 0.0f;
 
 __device__ __forceinline__ float neg_inf() { return -__int_as_float(0x7f800000); }
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
@@ -678,8 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_block_sparse_kernel(const __
         }
         if (mask) chain(0);
         chain(64);
-        const float mx2 = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2;
-        const float ref = i == 0 ? mx2 : (mx2 > old + kRescaleThreshold ? mx2 : old);
+        const float top = fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), sl2, -kLift<F16>);
+        const float ref = i == 0 ? top : (top > old + kRescaleThreshold ? top : old);
         // a row that has seen only masked keys (reference -inf) has O = 0: it takes the new one without a rescale
         const bool res = ref != old && old != neg_inf();
         if (__any_sync(0xffffffffu, res)) {

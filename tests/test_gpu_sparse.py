@@ -707,6 +707,33 @@ def test_attention_wait_limit_reports_timeout_and_context_survives(H, Sq):
     check_attention(q, k, v, idx, count, 64, O, L)
 
 
+@pytest.mark.parametrize("ty", [BF, FP])
+@pytest.mark.parametrize("H", [1, 80])
+@pytest.mark.parametrize("heavy", [0, 33_000, 65_535])
+def test_attention_many_light_keys_keep_their_weight(ty, H, heavy):
+    """One key with nearly all the weight and 65,535 of a weight near 2^-25.4 each, below half of fp16's least step,
+    which together are 1.5e-3 of a row."""
+    D, Sk = 64, 65_536
+    q = torch.zeros(H, 1, D, dtype=ty, device="cuda")
+    k, v = torch.zeros(1, Sk, D, dtype=ty, device="cuda"), torch.ones(1, Sk, D, dtype=ty, device="cuda")
+    q[..., 0], k[..., 0] = 8.0, -17.625
+    k[0, heavy, 0], v[0, heavy] = 0.0, 0.0
+    idx = torch.arange(Sk // 64, dtype=torch.int32, device="cuda").expand(H, 1, -1).contiguous()
+    for oty in (ty, F32):
+        O, L, st = attend(q, k, v, idx, None, 64, oty=oty)
+        assert st == 0
+        n, w = Sk - 1, math.exp(-17.625)
+        ref = n * w / (1 + n * w)
+        # logits are exact; ex2 and the weights' sum as in check_attention.  A rounded weight is off by half a step:
+        # 2^-8 or 2^-11 of it, or, below fp16's normal range, 2^-25 of a scale on which the heaviest weight is at
+        # least 2^7
+        e = 2.0 ** -22 + Sk * 64 * 2.0 ** -24 / 32
+        o = ref * (HALF[ty] + 2 * e) + TINY[ty] * 2.0 ** -7 * n
+        bound = o + HALF[oty] * (ref + o) + TINY[oty]
+        assert float((O.double() - ref).abs().max()) <= bound, (float(O.double().mean()), ref)
+        assert float((L.double() - math.log1p(n * w)).abs().max()) <= e + 2.0 ** -22
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("H,S,D,dims,topk", [(2, 1000, 64, (24, 20, 20), 5), (16, 1024, 72, (36, 36), 8), (3, 2080, 128, (44, 42, 42), 9)])
 def test_session_from_projection_to_sparse_output(H, S, D, dims, topk):
