@@ -469,6 +469,7 @@ extern "C" int dt_attn_block_sparse(const dt_sparse_params* p, const void* Q, co
                                                                              {V, p->v, p->Hkv, p->Sk, 2},
                                                                              {O, p->o, p->H, p->Sq, osize}};
   for (const auto& x : t) {
+    if (x.rows == 0) continue;                                          // no keys: dense strides are {0, D}
     if ((x.heads > 1 && (x.s.head <= 0 || x.s.head >= (int64_t)1 << 39)) ||
         (x.rows > 1 && (x.s.row <= 0 || x.s.row >= (int64_t)1 << 39)))
       return DT_ERR_INVALID;

@@ -5,6 +5,7 @@ Tolerances are element-wise bounds from the arithmetic: a rounding to a 16-bit
 type is off by at most half a step (bf16 2^-8, fp16 2^-11 of the value, fp16
 below 2^-14 by 2^-25 absolutely), one to fp32 by 2^-24."""
 
+import ctypes
 import math
 import os
 import subprocess
@@ -611,6 +612,22 @@ def test_attention_empty_lists_no_counts_no_keys():
     O, L, st = attend(q, k, v, full, None, 64)        # no counts: every entry
     assert st == 0
     check_attention(q, k, v, full, torch.full((2, 2), 4, dtype=torch.int32), 64, O, L)
+
+
+def test_attention_no_keys_with_dense_strides():
+    """Dense strides {Sk * D, D} of no keys are {0, D}: they describe nothing, and refuse nothing."""
+    H, Sq, D = 4, 140, 64
+    q = randn(gen(38), H, Sq, D, dtype=BF)
+    O, L = torch.full_like(q, 9.0), torch.full((H, Sq), 9.0, device="cuda")
+    idx, count = torch.zeros(H, 2, 3, dtype=torch.int32, device="cuda"), torch.zeros(H, 2, dtype=torch.int32, device="cuda")
+    st = torch.zeros(4, dtype=torch.int32, device="cuda")
+    dense = dt.Strides(Sq * D, D)
+    p = dt.SparseParams(H, 2, Sq, 0, D, 64, 3, dt.DT_TYPE_BF16, dt.DT_TYPE_BF16, dense, dt.Strides(0, D), dt.Strides(0, D), dense)
+    res = dt.load().dt_attn_block_sparse(ctypes.byref(p), q.data_ptr(), None, None, idx.data_ptr(), count.data_ptr(),
+                                         O.data_ptr(), L.data_ptr(), st.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert res == dt.DT_OK and int(st[0]) == 0
+    assert bool((O == 0).all()) and bool(torch.isneginf(L).all())
 
 
 def test_attention_strides_past_32_bits():
