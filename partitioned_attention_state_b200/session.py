@@ -56,6 +56,9 @@ class Session:
         self.group = group
         self.state_dtype = state_dtype
         self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            # this one from now on, whichever is current in later calls
+            self.device = torch.device("cuda", torch.cuda.current_device())
         win = mode == DT_MODE_WINDOW
         p = params(H, S, D, P if not win else 1, mode, reuse_per_row, window, 1, group)
         self.nqt, self.nseg = dt_plan_geometry(p)
@@ -137,10 +140,12 @@ class Session:
         self._measured = self._captured = None
 
     def _on(self, stream):
-        """Context in which `stream` (a torch stream, a raw handle, None: as it is) is the current one.  What a call
-        allocates for launches on `stream` has to come from that stream's pool: memory handed out on another one may
-        still be read by work that is pending there."""
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        """Context in which `stream` (a torch stream, a raw handle, None: the session's device's current one) is the
+        current one.  What a call allocates for launches on `stream` has to come from that stream's pool: memory handed
+        out on another one may still be read by work that is pending there."""
+        if stream is None:
+            return torch.cuda.device(self.device)
+        if not isinstance(stream, torch.cuda.Stream):
             raw = getattr(stream, "cuda_stream", stream)
             stream = torch.cuda.ExternalStream(raw, self.device) if raw else torch.cuda.default_stream(self.device)
         return torch.cuda.stream(stream)
@@ -154,6 +159,8 @@ class Session:
         self.q_mean, self.k_mean = self._means[k_block]
 
     def _capturing(self, stream) -> bool:
+        if stream is None and torch.cuda.current_device() == self.device.index:
+            return torch.cuda.is_current_stream_capturing()
         with self._on(stream):
             return torch.cuda.is_current_stream_capturing()
 

@@ -956,6 +956,18 @@ def test_session_block_means_of_captured_projections():
         Session(H, S, D, P=2, cache=False).declare_means(64)      # never measured
 
 
+@pytest.mark.parametrize("device", ["cuda", "cuda:0", torch.device("cuda", 0)])
+def test_session_keeps_the_device_it_was_made_on(device):
+    """"cuda" means the device that is current now, also for buffers allocated by later calls."""
+    with torch.cuda.device(0):
+        sess = Session(2, 300, 64, P=2, device=device, cache=False)
+    assert sess.device == sess.Q.device == torch.device("cuda", 0)
+    sess.set_inputs(*(randn(gen(97), 2, 300, 64, dtype=BF) for _ in range(3)))
+    sess.step_sparse(2)
+    sess.check()
+    assert sess.q_mean.device == sess.lists[0].device == sess.device
+
+
 # ------------------------------------------------------------------ fp32 states
 def attend_f32(q, k, v, idx, count, block, token_major):
     """O as fp32, dense or token-major (head-major view of [Sq][H][D])."""
