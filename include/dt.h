@@ -513,7 +513,10 @@ typedef struct {
  * blocks idx[h][s/128][0 .. count-1] (block j = rows [j*k_block, min((j+1)*
  * k_block, Sk))): OUT = softmax(q K^T / sqrt(D)) V and its natural-log LSE, a
  * state that composes with any other.  A row with an empty list gets (0,
- * -inf).  A block listed twice counts twice; any order is allowed.
+ * -inf).  A block listed twice counts twice; any order is allowed.  The
+ * softmax weights are rounded to the inputs' 16-bit type for the tensor cores
+ * (by at most 2^-8 of a weight in bf16, 2^-11 in fp16), with out_type fp32 too;
+ * logits, maxima, sums and the accumulation are fp32.
  *   Q, O     [H][Sq][D], K, V [Hkv][Sk][D], strides p->q, p->o, p->k, p->v
  *   idx      int32 [H][ceil(Sq/128)][cap] (device, read)
  *   count    int32 [H][ceil(Sq/128)] (device, read), or NULL: cap entries each
@@ -521,8 +524,8 @@ typedef struct {
  *   d_status int32 device status word (see conventions).  A count outside
  *            [0, cap] is clamped and an entry outside [0, ceil(Sk/k_block))
  *            contributes nothing; both write DT_ERR_INVALID to it
- * Row starts must be 16-byte aligned (pointers and strides); strides > 0, and
- * those of Q, K and V below 2^40 bytes.
+ * Row starts must be 16-byte aligned (pointers and strides); strides > 0 and
+ * below 2^39 elements; O and L overlap no input.
  * With few query blocks the CTAs of a cluster split each list and join their
  * states through distributed shared memory: one launch, no workspace, and the
  * same result run to run.  The waits of dt_set_wait_limit_ns span whole lists:

@@ -983,8 +983,13 @@ int launch_dp(SparseParams& p, int sms, cudaStream_t stream) {
     ready[dev].store(true, std::memory_order_release);
   }
   const int64_t items = (int64_t)p.H * p.nqb;
-  // Split the lists where whole lists would leave SMs idle: the largest
-  // cluster of which all run at once, at no less than two tiles a CTA.
+  // Split the lists where whole lists would leave half the SMs idle: the
+  // largest cluster of which all run at once, at no less than two tiles a CTA.
+  // One row a head over 512 blocks of 64, D = 128, 148 SMs: 40 heads 108 us in
+  // three, 129 in two, 148 in four (whose clusters do not all run at once), 219
+  // whole; 74 heads 182 in two, 203 in three, 237 whole.  With more lists than
+  // half the SMs the clusters come in waves: 75 heads 238 whole, 284 in two, 204
+  // in three; 100 heads 257, 292, 302; 148 heads 348, 357, 412.
   p.split = 1;
   const int tiles = ceil_div(p.cap, p.per_tile);
   if (2 * items <= sms)

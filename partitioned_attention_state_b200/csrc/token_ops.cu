@@ -338,7 +338,8 @@ __global__ void __launch_bounds__(kNormThreads, 3) qk_norm_rope_kernel(const __g
           --tleft;
         }
       if (sums) {
-        // (each lane overwrites its own slots, and every copy into them has been waited for or was never started)
+        // The second sums take the place of the rows.  A lane's 32 bytes lie over other lanes' 16-byte slots too: every
+        // lane waits for its own copies and all lanes meet before any writes.
         if (t0 > 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (t0 > 0) __syncwarp();
         float* dst = (t0 > 0 ? reinterpret_cast<float*>(rings + warp * M::kRing) : part + warp * 256) + 8 * l32;
@@ -720,8 +721,10 @@ int launch_qk_norm_rope(NormRopeArgs a, int sms, cudaStream_t stream) {
 int launch_block_select(const dt_select_params& p, const float* q_mean, const float* k_mean, int32_t* idx,
                         int32_t* count, cudaStream_t stream) {
   // Query blocks per CTA: as many as there are, up to 8, while the keys of the rows leave room for four CTAs on an SM
-  // (some score while others select: 75 us on 40 heads of 256 x 512 blocks at D = 128, against 79 with 16 rows and
-  // two CTAs); longer rows take what they need.
+  // (some score while others select), and one at the least.  Measured at D = 128: 40 heads of 256 x 512 blocks 76 us
+  // with 8 rows, 124 with 4, 217 with 2, and 79 with 16 rows on two CTAs an SM.  Rows of a thousand blocks and more
+  // get fewer than is best: 16 x 1,024 blocks 39 us with the 4 of this rule, 31 with 8; 16 x 3,000 206 with 1, 130
+  // with 2; 32 x 4,096 475 with 1, 341 with 4; 16 heads of 128 x 8,192 1,729 with 1, 1,517 with 2.
   int R = kSelRows;
   while (R > 1 && (R / 2 >= p.nq || select_smem(R, p.D, p.nk) > 46 * 1024)) R /= 2;
   const size_t smem = select_smem(R, p.D, p.nk);
